@@ -20,6 +20,9 @@ __all__ = [
     "fa_fwd_standard", "fa_fwd_standard_workspace_size", "attention_forward_standard",
     "fa_watchdog_selftest", "attention_forward", "attention_backward", "attention_forward_fp8", "lib",
     "STATUS_NAMES", "STATUS_CODES", "strerror",
+    "ROPE_SCALINGS", "rope_frequencies", "fa_rope", "rope_forward", "rope_backward", "fa_page_tables",
+    "fa_cache_append_fp8", "fa_fwd_decode_paged_fp8", "fa_fwd_decode_paged_fp8_workspace_size",
+    "attention_decode_paged_fp8",
 ]
 
 
@@ -270,3 +273,169 @@ def attention_backward_fp8(q8, k8, v8, q_descale, k_descale, v_descale, o, do, l
     fa_bwd_fp8(q8, k8, v8, q_descale, k_descale, v_descale, o, do, lse, dq, dk, dv,
                _default_scale(d) if scale is None else scale, causal, workspace, stream)
     return dq, dk, dv
+
+
+# ------------------------------------------------- serving over an 8-bit paged cache, and rotary positions
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _on_device(fn, device, stream, *args):
+    """Calls fn(*args, stream) with `device` current, on `stream` or that device's current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return check(fn(*args, (stream or torch.cuda.current_stream()).cuda_stream))
+    return check(fn(*args, (stream or torch.cuda.current_stream()).cuda_stream))
+
+
+def _check_as(t, name, shape, dtypes, device):
+    if t.device != device or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {' or '.join(str(x) for x in dtypes)} {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _cuda_device(t):
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    return t.device
+
+
+_I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: float = 0.0, low: float = 1.0, high: float = 4.0, device="cuda"):
+    """(inv_freq, attention factor) of rotary positions: inv_freq is an fp64 tensor [rot_dim / 2] on `device`,
+    radians per position.  scaling is a key of ROPE_SCALINGS (see fa_rope_scaling in fa.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = (ctypes.c_double * max(1, rot_dim // 2))()
+    att = ctypes.c_double()
+    check(lib.fa_rope_frequencies(out, ctypes.byref(att), rot_dim, base, ROPE_SCALINGS[scaling], factor,
+                                  original_length, low, high))
+    return torch.tensor(list(out), dtype=torch.float64, device=device), att.value
+
+
+def fa_rope(x, y, positions, inv_freq, factor: float = 1.0, interleaved: bool = False, transpose: bool = False,
+            stream=None) -> None:
+    """y <- x [B,H,N,d] bf16 with rotary positions on its first 2 * len(inv_freq) elements.  x and y may have any
+    batch, head and token strides (d contiguous); y may be x.  positions: int32 [B,N], or None for 0..N-1."""
+    B, H, N, d = _shape(x)
+    dev = _cuda_device(x)
+    for t in (x, y):
+        if t.dtype != torch.bfloat16 or t.shape != x.shape or t.device != dev or (t.stride(3) != 1 and d > 1):
+            raise ValueError(f"expected bf16 {tuple(x.shape)} on {dev} with d contiguous, got {t.dtype} {tuple(t.shape)}")
+    if positions is not None:
+        _check_as(positions, "positions", (B, N), _I32, dev)
+    _check_as(inv_freq, "inv_freq", (inv_freq.numel(),), (torch.float64,), dev)
+    xs = (ctypes.c_longlong * 3)(*x.stride()[:3])
+    ys = (ctypes.c_longlong * 3)(*y.stride()[:3])
+    _on_device(lib.fa_rope, dev, stream, x.data_ptr(), y.data_ptr(), _ptr(positions), inv_freq.data_ptr(), factor,
+               B, H, N, d, 2 * inv_freq.numel(), int(bool(interleaved)), int(bool(transpose)), xs, ys)
+
+
+def rope_forward(x, positions, inv_freq, interleaved: bool = False, factor: float = 1.0, stream=None):
+    """Rotary positions on x, as a new contiguous tensor."""
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    fa_rope(x, y, positions, inv_freq, factor, interleaved, False, stream)
+    return y
+
+
+def rope_backward(dy, positions, inv_freq, interleaved: bool = False, factor: float = 1.0, stream=None):
+    """Gradient of rope_forward with respect to x, as a new contiguous tensor."""
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    fa_rope(dy, dx, positions, inv_freq, factor, interleaved, True, stream)
+    return dx
+
+
+def fa_page_tables(ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens,
+                   free_head_out, page_size: int, stream=None) -> None:
+    """Grows (new_lens >= 0) or finishes (new_lens < 0) the requests of a batch: takes pages from free_pages,
+    writes block_table, slots, positions, seq_lens and free_head_out.  All int32; seq_lens may be ctx_lens and
+    free_head_out may be free_head."""
+    dev = _cuda_device(ctx_lens)
+    if slots.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("slots must be [B, N] and block_table [B, max_pages]")
+    B, N = slots.shape
+    max_pages = block_table.shape[1]
+    n_free = free_pages.numel()
+    for t, name, shape in ((ctx_lens, "ctx_lens", (B,)), (new_lens, "new_lens", (B,)),
+                           (free_pages, "free_pages", (n_free,)), (free_head, "free_head", (1,)),
+                           (block_table, "block_table", (B, max_pages)), (slots, "slots", (B, N)),
+                           (positions, "positions", (B, N)), (seq_lens, "seq_lens", (B,)),
+                           (free_head_out, "free_head_out", (1,))):
+        _check_as(t, name, shape, _I32, dev)
+    _on_device(lib.fa_page_tables, dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+               free_head.data_ptr(), block_table.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+               seq_lens.data_ptr(), free_head_out.data_ptr(), B, N, n_free, max_pages, page_size)
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev):
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d]")
+    pages, page = k_cache.shape[0], k_cache.shape[2]
+    _check_as(k_cache, "k_cache", (pages, Hkv, page, d), _E4M3, dev)
+    _check_as(v_cache, "v_cache", (pages, Hkv, page, d), _E4M3, dev)
+    _check_as(k_scale, "k_scale", (pages, Hkv), _F32, dev)
+    _check_as(v_scale, "v_scale", (pages, Hkv), _F32, dev)
+    return pages, page
+
+
+def fa_cache_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
+    """Quantises k, v [B,Hkv,N,d] bf16 into the pages that slots [B,N] int32 names (negative: not written);
+    k_cache, v_cache e4m3 [num_pages,Hkv,page_size,d], k_scale, v_scale fp32 [num_pages,Hkv]."""
+    B, Hkv, N, d = _shape(k)
+    dev = _cuda_device(k)
+    _check_as(k, "k", (B, Hkv, N, d), _BF16, dev)
+    _check_as(v, "v", (B, Hkv, N, d), _BF16, dev)
+    _check_as(slots, "slots", (B, N), _I32, dev)
+    pages, page = _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    _on_device(lib.fa_cache_append_fp8, dev, stream, k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
+               v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, Hkv, N, d, pages, page)
+
+
+def fa_fwd_decode_paged_fp8_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int) -> int:
+    n = int(lib.fa_fwd_decode_paged_fp8_workspace_size(B, H, Hkv, Nq, d))
+    if n == ctypes.c_size_t(-1).value:
+        raise FAError(1, "invalid shape for fa_fwd_decode_paged_fp8_workspace_size")
+    return n
+
+
+def fa_fwd_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, scale: float,
+                            causal: bool, workspace, stream=None) -> None:
+    """O, LSE <- attention of q [B,H,Nq,d] (Nq <= 16) over the first seq_lens[b] tokens of each request's pages;
+    block_table int32 [B,max_pages], seq_lens int32 [B], caches and scales as in fa_cache_append_fp8."""
+    B, H, Nq, d = _shape(q)
+    dev = _cuda_device(q)
+    _check_as(q, "q", (B, H, Nq, d), _BF16, dev)
+    _check_as(o, "o", (B, H, Nq, d), _BF16, dev)
+    _check_as(lse, "lse", (B, H, Nq), _F32, dev)
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d] and block_table [B, max_pages]")
+    Hkv = k_cache.shape[1]
+    pages, page = _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    max_pages = block_table.shape[1]
+    _check_as(block_table, "block_table", (B, max_pages), _I32, dev)
+    _check_as(seq_lens, "seq_lens", (B,), _I32, dev)
+    wptr, wbytes = 0, 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        wptr, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _on_device(lib.fa_fwd_decode_paged_fp8, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+               k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+               lse.data_ptr(), B, H, Hkv, Nq, d, pages, page, max_pages, float(scale), int(bool(causal)), wptr, wbytes)
+
+
+def attention_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                               scale: float | None = None, causal: bool = False, workspace=None, stream=None):
+    """Allocates O, LSE (and the workspace unless given) with torch and runs fa_fwd_decode_paged_fp8."""
+    B, H, Nq, d = _shape(q)
+    o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        n = fa_fwd_decode_paged_fp8_workspace_size(B, H, k_cache.shape[1], Nq, d)
+        workspace = torch.empty(max(16, n), dtype=torch.uint8, device=q.device)
+    fa_fwd_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse,
+                            _default_scale(d) if scale is None else scale, causal, workspace, stream)
+    return o, lse

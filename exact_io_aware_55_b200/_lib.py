@@ -23,6 +23,7 @@ STATUS_NAMES = {
     6: "FA_ERR_DEVICE_TIMEOUT",
     7: "FA_ERR_WORKSPACE",
     8: "FA_ERR_SCRATCH_LIMIT",
+    9: "FA_ERR_BAD_PAGE",
 }
 STATUS_CODES = {v: k for k, v in STATUS_NAMES.items()}
 
@@ -75,6 +76,20 @@ def _load() -> ctypes.CDLL:
     lib.fa_bwd_noalloc.restype = i
     lib.fa_bwd_noalloc_max_bytes.argtypes = []
     lib.fa_bwd_noalloc_max_bytes.restype = sz
+    dbl, ll = ctypes.c_double, ctypes.c_longlong
+    lib.fa_rope_frequencies.argtypes = [ctypes.POINTER(dbl), ctypes.POINTER(dbl), i, dbl, i, dbl, dbl, dbl, dbl]
+    lib.fa_rope_frequencies.restype = i
+    lib.fa_rope.argtypes = [vp, vp, vp, vp, f, i, i, i, i, i, i, i, ctypes.POINTER(ll), ctypes.POINTER(ll), vp]
+    lib.fa_rope.restype = i
+    lib.fa_page_tables.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
+    lib.fa_page_tables.restype = i
+    lib.fa_cache_append_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp]
+    lib.fa_cache_append_fp8.restype = i
+    lib.fa_fwd_decode_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, vp, sz,
+                                            vp]
+    lib.fa_fwd_decode_paged_fp8.restype = i
+    lib.fa_fwd_decode_paged_fp8_workspace_size.argtypes = [i, i, i, i, i]
+    lib.fa_fwd_decode_paged_fp8_workspace_size.restype = sz
     lib.fa_strerror.argtypes = [i]
     lib.fa_strerror.restype = ctypes.c_char_p
     lib.fa_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]

@@ -20,7 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa.so")
-SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd64.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_decode.cu", "fa_standard.cu", "fa_noalloc.cu"]
+SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd64.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_decode.cu", "fa_standard.cu", "fa_noalloc.cu",
+           "fa_rope.cu", "fa_cache.cu", "fa_decode_paged.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "-cudart", "static"]

@@ -584,6 +584,221 @@ fa_status fa_fwd_standard(const void* q, const void* k, const void* v, void* o, 
   return launch_status(fa::launch_standard(tq, tk, tv, tp, a, d, static_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// Shape checks of the calls on the 8-bit paged cache and of fa_rope.
+bool page_ok(int page_size) { return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128; }
+
+// num_pages * Hkv rows of page_size * d bytes: the tensor maps index
+// (page, head) pairs and a slot in 32 bits.
+bool cache_fits(int num_pages, int Hkv, int page_size) {
+  return static_cast<long long>(num_pages) * Hkv <= 0x7fffffffll &&
+         static_cast<long long>(num_pages) * page_size <= 0x7fffffffll;
+}
+
+fa_status check_paged(int B, int H, int Hkv, int Nq, int d, float scale, int causal, bool* empty) {
+  if (B < 0 || H < 0 || Hkv < 0 || Nq < 0) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale >= 0.0f)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (Nq > kDecodeMaxNq) return FA_ERR_UNSUPPORTED;
+  *empty = B == 0 || H == 0 || Nq == 0;
+  if (*empty) return FA_OK;
+  if (Hkv == 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * H > 65535) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rope_frequencies(double* inv_freq, double* attention_factor, int rot_dim, double base, int scaling,
+                              double factor, double original_length, double low, double high) {
+  if (!inv_freq || !attention_factor || rot_dim < 2 || rot_dim % 2 != 0) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(base) && base > 1.0)) return FA_ERR_INVALID_ARG;
+  if (scaling < FA_ROPE_NONE || scaling > FA_ROPE_BANDS) return FA_ERR_INVALID_ARG;
+  if (scaling != FA_ROPE_NONE && !(std::isfinite(factor) && factor >= 1.0)) return FA_ERR_INVALID_ARG;
+  const bool by_turns = scaling == FA_ROPE_YARN || scaling == FA_ROPE_BANDS;
+  if (by_turns && !(std::isfinite(original_length) && original_length >= 1.0 && std::isfinite(high) && low > 0.0 &&
+                    high > low))
+    return FA_ERR_INVALID_ARG;
+  if (scaling == FA_ROPE_NTK && rot_dim == 2) return FA_ERR_INVALID_ARG;   // the exponent's pole
+  const double two_pi = 6.283185307179586476925;
+  const double b = scaling == FA_ROPE_NTK ? base * std::pow(factor, rot_dim / (rot_dim - 2.0)) : base;
+  double first = 0.0, last = 0.0;
+  if (scaling == FA_ROPE_YARN) {   // the pair that makes t turns within original_length
+    const auto pair_of = [&](double t) {
+      return rot_dim * std::log(original_length / (t * two_pi)) / (2.0 * std::log(base));
+    };
+    first = std::max(std::floor(pair_of(high)), 0.0);
+    last = std::min(std::ceil(pair_of(low)), rot_dim - 1.0);
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = std::pow(b, -2.0 * i / rot_dim);
+    double keep = 1.0;             // share of the unscaled frequency
+    if (scaling == FA_ROPE_LINEAR) keep = 0.0;
+    if (scaling == FA_ROPE_YARN) keep = 1.0 - std::min(std::max((i - first) / std::max(last - first, 1e-3), 0.0), 1.0);
+    if (scaling == FA_ROPE_BANDS)
+      keep = std::min(std::max((original_length * f / two_pi - low) / (high - low), 0.0), 1.0);
+    inv_freq[i] = scaling == FA_ROPE_NONE || scaling == FA_ROPE_NTK ? f : f / factor * (1.0 - keep) + f * keep;
+  }
+  *attention_factor = scaling == FA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return FA_OK;
+}
+
+fa_status fa_rope(const void* x, void* y, const int* positions, const double* inv_freq, float factor, int B, int H,
+                  int N, int d, int rot_dim, int interleaved, int transpose, const long long* x_strides,
+                  const long long* y_strides, void* stream) {
+  if (B < 0 || H < 0 || N < 0) return FA_ERR_INVALID_ARG;
+  if ((interleaved != 0 && interleaved != 1) || (transpose != 0 && transpose != 1)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(factor)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * H > 65535 || static_cast<long long>(B) * N > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || H == 0 || N == 0) return FA_OK;
+  if (!x || !y || !inv_freq || !x_strides || !y_strides) return FA_ERR_INVALID_ARG;
+  const int sizes[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i) {
+    if (x_strides[i] < 0 || y_strides[i] < 0) return FA_ERR_INVALID_ARG;
+    if (sizes[i] > 1 && y_strides[i] < d) return FA_ERR_INVALID_ARG;      // rows of the output would overlap
+    if (x == y && sizes[i] > 1 && x_strides[i] != y_strides[i]) return FA_ERR_INVALID_ARG;
+    if (sizes[i] > 1 && (x_strides[i] % 8 != 0 || y_strides[i] % 8 != 0)) return FA_ERR_ALIGNMENT;
+  }
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(inv_freq, 8) || !aligned(positions, 4)) return FA_ERR_ALIGNMENT;
+  uint32_t* status = nullptr;
+  const fa_status st = current_device(&status);
+  if (st != FA_OK) return st;
+  fa::RopeArgs a{};
+  a.x = x;
+  a.y = y;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.factor = factor;
+  a.sin_factor = transpose ? -factor : factor;
+  a.B = B;
+  a.H = H;
+  a.N = N;
+  a.d = d;
+  a.rot_dim = rot_dim;
+  a.in_place = x == y;
+  for (int i = 0; i < 3; ++i) {
+    a.xs[i] = sizes[i] > 1 ? x_strides[i] : 0;
+    a.ys[i] = sizes[i] > 1 ? y_strides[i] : 0;
+  }
+  return launch_status(fa::launch_rope(a, interleaved != 0, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_page_tables(const int* ctx_lens, const int* new_lens, int* free_pages, const int* free_head,
+                         int* block_table, int* slots, int* positions, int* seq_lens, int* free_head_out, int B,
+                         int N, int n_free, int max_pages, int page_size, void* stream) {
+  if (B < 0 || N < 0 || n_free < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
+  if (!page_ok(page_size)) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || static_cast<long long>(max_pages) * page_size > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  if (B == 0) return FA_OK;
+  if (!ctx_lens || !new_lens || !free_head || !seq_lens || !free_head_out) return FA_ERR_INVALID_ARG;
+  if ((N > 0 && (!slots || !positions)) || (n_free > 0 && !free_pages) || (max_pages > 0 && !block_table))
+    return FA_ERR_INVALID_ARG;
+  const void* every[] = {ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens, free_head_out};
+  for (const void* p : every)
+    if (!aligned(p, 4)) return FA_ERR_ALIGNMENT;
+  uint32_t* status = nullptr;
+  const fa_status st = current_device(&status);
+  if (st != FA_OK) return st;
+  const fa::TableArgs a{status, ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens,
+                        free_head_out, B, N, n_free, max_pages, page_size};
+  return launch_status(fa::launch_page_tables(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache_append_fp8(const void* k, const void* v, const int* slots, void* k_cache, void* v_cache,
+                              float* k_scale, float* v_scale, int B, int Hkv, int N, int d, int num_pages,
+                              int page_size, void* stream) {
+  if (B < 0 || Hkv < 0 || N < 0 || num_pages < 0) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (!page_ok(page_size)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv > 65535 || static_cast<long long>(B) * N > 0x7fffffffll ||
+      !cache_fits(num_pages, Hkv, page_size))
+    return FA_ERR_UNSUPPORTED;
+  if (B == 0 || Hkv == 0 || N == 0) return FA_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return FA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 4) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return FA_ERR_ALIGNMENT;
+  uint32_t* status = nullptr;
+  const fa_status st = current_device(&status);
+  if (st != FA_OK) return st;
+  fa::AppendArgs a{};
+  a.status = status;
+  a.k = k;
+  a.v = v;
+  a.slots = slots;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.N = N;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  return launch_status(fa::launch_cache_append(a, d, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_fwd_decode_paged_fp8_workspace_size(int B, int H, int Hkv, int Nq, int d) {
+  bool empty = false;
+  if (check_paged(B, H, Hkv, Nq, d, 1.0f, 0, &empty) != FA_OK) return static_cast<size_t>(-1);
+  return 0;
+}
+
+fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                  const float* v_scale, const int* block_table, const int* seq_lens, void* o,
+                                  float* lse, int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size,
+                                  int max_pages, float scale, int causal, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  bool empty = false;
+  fa_status st = check_paged(B, H, Hkv, Nq, d, scale, causal, &empty);
+  if (st != FA_OK) return st;
+  if (num_pages < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
+  if (!page_ok(page_size)) return FA_ERR_UNSUPPORTED;
+  if (empty) return FA_OK;
+  if (!cache_fits(num_pages, Hkv, page_size) || static_cast<long long>(max_pages) * page_size > (1ll << 30))
+    return FA_ERR_UNSUPPORTED;
+  if (!q || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
+  if ((max_pages > 0 && !block_table) || (num_pages > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)))
+    return FA_ERR_INVALID_ARG;
+  const size_t need = fa_fwd_decode_paged_fp8_workspace_size(B, H, Hkv, Nq, d);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(workspace, 16))
+    return FA_ERR_ALIGNMENT;
+  uint32_t* status = nullptr;
+  if ((st = current_device(&status)) != FA_OK) return st;
+  fa::PagedArgs a{};
+  a.status = status;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.o = o;
+  a.lse = lse;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.Nq = Nq;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.max_pages = num_pages > 0 ? max_pages : 0;
+  a.causal = causal;
+  a.c_log2 = scale * kLog2e;
+  return launch_status(fa::launch_decode_paged(a, d, static_cast<cudaStream_t>(stream)));
+}
+
 const char* fa_strerror(fa_status s) {
   switch (s) {
     case FA_OK: return "ok";
@@ -598,6 +813,7 @@ const char* fa_strerror(fa_status s) {
     case FA_ERR_WORKSPACE: return "backward workspace missing or smaller than fa_bwd_workspace_size()";
     case FA_ERR_SCRATCH_LIMIT:
       return "shape needs more backward scratch than fa_bwd_noalloc's fixed array (fa_bwd_noalloc_max_bytes())";
+    case FA_ERR_BAD_PAGE: return "a kernel met a page or slot outside the cache and skipped it";
   }
   return "unknown fa_status";
 }
@@ -612,6 +828,7 @@ fa_status fa_device_status(void* stream, uint32_t* where) {
   if (cudaMemsetAsync(status, 0, sizeof(host), s) != cudaSuccess) return FA_ERR_LAUNCH;
   if (cudaStreamSynchronize(s) != cudaSuccess) return FA_ERR_LAUNCH;
   if (where) *where = host[1];
+  if (host[0] == fa::DEVSTATUS_BAD_PAGE) return FA_ERR_BAD_PAGE;
   return host[0] == 0u ? FA_OK : FA_ERR_DEVICE_TIMEOUT;
 }
 

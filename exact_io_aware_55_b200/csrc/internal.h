@@ -59,6 +59,10 @@ enum WaitSite : uint32_t {
   WAIT_STD_PV_EMPTY = 66,
   WAIT_STD_PV_FULL = 67,
   WAIT_STD_PV_DONE = 68,
+  // sites that report a page or slot outside the cache
+  WAIT_APPEND_SLOT = 80,
+  WAIT_TABLES_BACK = 81,
+  WAIT_PAGED_TABLE = 82,
   WAIT_SELFTEST = 99,
 };
 
@@ -176,6 +180,75 @@ cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
 template <int D, bool CAUSAL>
 cudaError_t launch_bwd_dq(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
+
+// Rotary positions on [B, H, N, d] bf16 (fa_rope.cu).
+struct RopeArgs {
+  const void* x;
+  void* y;
+  const int* positions;    // [B, N], or NULL: token n of a sequence is at position n
+  const double* inv_freq;  // [rot_dim / 2], radians per position
+  float factor;            // on the cosines
+  float sin_factor;        // on the sines: factor, or -factor for the transposed rotation
+  int B, H, N, d;
+  int rot_dim;
+  bool in_place;           // y is x: what is not turned stays
+  long long xs[3], ys[3];  // element strides of batch, head and token
+  int heads_per_thread;    // set by the launcher
+};
+cudaError_t launch_rope(RopeArgs a, bool interleaved, cudaStream_t stream);
+
+// Write of new tokens into the 8-bit paged cache (fa_cache.cu).
+struct AppendArgs {
+  uint32_t* status;
+  const void* k;       // bf16 [B, Hkv, N, d]
+  const void* v;
+  const int* slots;    // [B, N]: page * page size + offset, negative: not written
+  void* k_cache;       // e4m3 [num_pages, Hkv, page, d]
+  void* v_cache;
+  float* k_scale;      // [num_pages, Hkv]
+  float* v_scale;
+  int B, Hkv, N;
+  int num_pages;
+  int page;
+  int window, windows, heads_per_block;   // set by the launcher
+};
+cudaError_t launch_cache_append(const AppendArgs& a, int d, cudaStream_t stream);
+
+// Page tables, slot maps and positions from request lengths (fa_cache.cu).
+struct TableArgs {
+  uint32_t* status;
+  const int* ctx_lens;   // [B]; may be seq_lens
+  const int* new_lens;   // [B]
+  int* free_pages;       // [n_free], in use from *free_head on
+  const int* free_head;  // may be free_head_out
+  int* block_table;      // [B, max_pages]
+  int* slots;            // [B, N]
+  int* positions;        // [B, N]
+  int* seq_lens;         // [B]
+  int* free_head_out;
+  int B, N, n_free, max_pages, page;
+};
+cudaError_t launch_page_tables(const TableArgs& a, cudaStream_t stream);
+
+// Attention over the 8-bit paged cache (fa_decode_paged.cu).
+struct PagedArgs {
+  uint32_t* status;
+  const void* q;            // bf16 [B, H, Nq, d]
+  const void* k_cache;      // e4m3 [num_pages, Hkv, page, d]
+  const void* v_cache;
+  const float* k_scale;     // [num_pages, Hkv]
+  const float* v_scale;
+  const int* block_table;   // [B, max_pages]
+  const int* seq_lens;      // [B]
+  void* o;                  // bf16 [B, H, Nq, d]
+  float* lse;               // [B, H, Nq]
+  int B, H, Hkv, Nq;
+  int num_pages, page, max_pages;
+  int causal;
+  float c_log2;             // scale * log2(e)
+};
+cudaError_t launch_decode_paged(const PagedArgs& a, int d, cudaStream_t stream);
+
 cudaError_t launch_watchdog_selftest(uint64_t limit_ns, cudaStream_t stream);
 
 }  // namespace fa

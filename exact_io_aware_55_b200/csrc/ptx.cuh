@@ -16,7 +16,13 @@ namespace fa {
 enum : uint32_t {
   DEVSTATUS_OK = 0,
   DEVSTATUS_WAIT_TIMEOUT = 1,
+  DEVSTATUS_BAD_PAGE = 2,       // a page or slot outside the cache was skipped
 };
+
+// Records a status unless one is recorded already.
+__device__ __forceinline__ void report_status(uint32_t* status, uint32_t code, uint32_t where) {
+  if (atomicCAS(&status[0], DEVSTATUS_OK, code) == DEVSTATUS_OK) atomicExch(&status[1], where);
+}
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 #ifndef FA_WAIT_LIMIT_NS

@@ -72,7 +72,8 @@ typedef enum fa_status {
   FA_ERR_LAUNCH = 5,          /* CUDA runtime rejected a launch or attribute */
   FA_ERR_DEVICE_TIMEOUT = 6,  /* a bounded device wait ran out (fa_device_status) */
   FA_ERR_WORKSPACE = 7,       /* backward workspace missing or too small */
-  FA_ERR_SCRATCH_LIMIT = 8    /* shape needs more than fa_bwd_noalloc's fixed scratch */
+  FA_ERR_SCRATCH_LIMIT = 8,   /* shape needs more than fa_bwd_noalloc's fixed scratch */
+  FA_ERR_BAD_PAGE = 9         /* a kernel met a page or slot outside the cache and skipped it (fa_device_status) */
 } fa_status;
 
 /*
@@ -286,6 +287,146 @@ FA_API fa_status fa_fwd_standard(const void* q, const void* k, const void* v, vo
 /* Bytes of workspace fa_fwd_standard needs ((size_t)-1 for invalid arguments). */
 FA_API size_t fa_fwd_standard_workspace_size(int B, int H, int N, int d);
 
+/*
+ * Serving over an 8-bit paged KV cache: fa_page_tables, fa_rope,
+ * fa_cache_append_fp8 and fa_fwd_decode_paged_fp8 are a decode step's calls
+ * around the model's projections (chipfoundryservices glossary "flash
+ * attention", closing section: inference against a KV cache).
+ *
+ * The cache.  A page holds page_size (16, 32, 64 or 128) tokens of every KV
+ * head: k_cache and v_cache are e4m3 [num_pages, Hkv, page_size, d], and each
+ * page and head has one scale, k_scale and v_scale fp32 [num_pages, Hkv]; a
+ * stored value is code * scale.  block_table int32 [B, max_pages] lists each
+ * request's pages in order, a slot is page * page_size + row of the page.
+ * All lengths and tables are device memory that the kernels read: a step can
+ * be captured into a CUDA graph and replayed as the lengths grow.
+ *
+ * What the host cannot check is checked by the kernels: a length below zero
+ * or beyond the table counts as the nearest possible one; a page or slot
+ * outside the cache is skipped (its keys count as not visible) and
+ * fa_device_status then returns FA_ERR_BAD_PAGE.
+ */
+
+/* Scalings of the rotary frequencies f_i = base^(-2 i / rot_dim). */
+typedef enum fa_rope_scaling {
+  FA_ROPE_NONE = 0,    /* f_i */
+  FA_ROPE_LINEAR = 1,  /* f_i / factor: positions interpolated */
+  FA_ROPE_NTK = 2,     /* the base raised to base * factor^(rot_dim / (rot_dim - 2)) */
+  FA_ROPE_YARN = 3,    /* between f_i / factor and f_i by a ramp over i, whose ends are the pairs that make `high`
+                          and `low` turns within original_length; the rotation is multiplied by 0.1 ln(factor) + 1 */
+  FA_ROPE_BANDS = 4    /* between f_i / factor and f_i by the number of turns within original_length: f_i / factor
+                          up to `low` turns, f_i from `high` turns on, linear in between */
+} fa_rope_scaling;
+
+/*
+ * Rotary frequencies of rot_dim / 2 pairs, computed on the host in 64 bits
+ * (no GPU involved): inv_freq[i] in radians per position, *attention_factor
+ * the factor of the rotation (1 but for FA_ROPE_YARN).  factor >= 1;
+ * original_length, low and high are used by FA_ROPE_YARN and FA_ROPE_BANDS
+ * (0 < low < high).  The caller copies inv_freq to the device once.
+ */
+FA_API fa_status fa_rope_frequencies(double* inv_freq, double* attention_factor, int rot_dim, double base,
+                                     int scaling, double factor, double original_length, double low, double high);
+
+/*
+ * Rotary positions: turns each pair (u, w) of the first rot_dim elements of
+ * every head row by a = position * inv_freq[pair],
+ *   u' = factor * (u cos a - w sin a),  w' = factor * (w cos a + u sin a),
+ * and copies the other d - rot_dim elements.  transpose != 0 turns by -a: the
+ * gradient of the call with respect to x, applied to the gradient of y.
+ *   x, y        : in/out, bf16 [B,H,N,d] with strides: x_strides and y_strides
+ *                 (host arrays) give the elements from one batch, head and
+ *                 token to the next; d is contiguous.  y may be x with equal
+ *                 strides (in place); otherwise they must not overlap.  An
+ *                 input may repeat rows (stride 0), an output may not.
+ *   positions   : in, int32 [B,N] (any value), or NULL for 0..N-1
+ *   inv_freq    : in, fp64 [rot_dim/2], device memory, 8-byte aligned
+ *   interleaved : pairs are elements (2i, 2i+1), else (i, i + rot_dim/2)
+ * rot_dim is a multiple of 16, at most d; strides are multiples of 8 elements.
+ * Angles are reduced in 64 bits, so positions of 10^6 and more keep their accuracy.
+ */
+FA_API fa_status fa_rope(const void* x, void* y, const int* positions, const double* inv_freq, float factor, int B,
+                         int H, int N, int d, int rot_dim, int interleaved, int transpose,
+                         const long long* x_strides, const long long* y_strides, void* stream);
+
+/*
+ * Page tables of a batch, built on the GPU from request lengths.  Request b
+ * holds ctx_lens[b] tokens and asks for new_lens[b] more (0..N), or has
+ * finished (new_lens[b] < 0).
+ *   1. The pages of finished requests go back, in order of the requests, in
+ *      front of the free ones: free_pages[*free_head ..] grows downwards.
+ *   2. Requests take the pages they need from the front, in order.  A request
+ *      is granted if it needs none or if the needs up to and with its own fit;
+ *      one that does not fit, that asks for more than N tokens or that would
+ *      not fit its row of the table keeps its length and gets no slot.
+ *   ctx_lens    : in,  int32 [B]
+ *   new_lens    : in,  int32 [B]
+ *   free_pages  : in/out, int32 [n_free]; free from index *free_head on
+ *   free_head   : in,  int32 [1], device memory
+ *   block_table : in/out, int32 [B, max_pages]; only the entries of pages that
+ *                 are taken are written (a finished request's row stays)
+ *   slots       : out, int32 [B,N]: slot of new token t, -1 where there is none
+ *   positions   : out, int32 [B,N]: ctx_lens[b] + t, 0 where there is none
+ *   seq_lens    : out, int32 [B]: new length (0 when finished); may be ctx_lens
+ *   free_head_out : out, int32 [1]; may be free_head
+ * A request was granted iff seq_lens[b] = ctx_lens[b] + new_lens[b].  N = 0
+ * only gives pages back.  If more pages come back than ever were taken
+ * (the returned ones exceed *free_head), none does and FA_ERR_BAD_PAGE is recorded.
+ */
+FA_API fa_status fa_page_tables(const int* ctx_lens, const int* new_lens, int* free_pages, const int* free_head,
+                                int* block_table, int* slots, int* positions, int* seq_lens, int* free_head_out,
+                                int B, int N, int n_free, int max_pages, int page_size, void* stream);
+
+/*
+ * Writes new keys and values into the 8-bit cache.
+ *   k, v    : in, bf16 [B,Hkv,N,d]
+ *   slots   : in, int32 [B,N]; a negative slot's token is not written
+ * Tokens of one request that follow one another on one page are quantised
+ * together, and a page is written by one such run only (a page that two runs
+ * name ends up with the codes of both under the scale of either).  Where two
+ * tokens of a run name one slot, the later one is stored.  With amax the
+ * largest finite absolute value of the run in that head:
+ *   e     = smallest exponent in [-60, 60] with amax <= 448 * 2^e (-60 for amax = 0)
+ *   scale = 2^e if the run writes the page's row 0 (the page starts anew, its
+ *           old codes and scale mean nothing), else max(old scale, 2^e)
+ *   code  = e4m3(x / scale), round to nearest even; what is not finite is
+ *           stored as NaN, what exceeds 448 * 2^60 as the largest value.
+ * If the scale grows, the page's other codes become e4m3(code * old / new).
+ * Scales are powers of two, so that step is exact down to the type's
+ * subnormals.  An old scale that is not positive and finite keeps nothing of
+ * the page (its other codes become 0).
+ */
+FA_API fa_status fa_cache_append_fp8(const void* k, const void* v, const int* slots, void* k_cache, void* v_cache,
+                                     float* k_scale, float* v_scale, int B, int Hkv, int N, int d, int num_pages,
+                                     int page_size, void* stream);
+
+/*
+ * Decode against the 8-bit paged cache: Nq (1..16) new queries of each head
+ * attend over the first seq_lens[b] tokens of request b (the queries' own
+ * tokens are in the cache and counted).  H is a multiple of Hkv; query heads
+ * h * H/Hkv .. (h+1) * H/Hkv - 1 share KV head h.
+ *   q           : in,  bf16 [B,H,Nq,d]
+ *   o           : out, bf16 [B,H,Nq,d]
+ *   lse         : out, fp32 [B,H,Nq], natural log
+ *   causal      : query i sees keys j <= seq_lens[b] - Nq + i
+ *   workspace   : >= fa_fwd_decode_paged_fp8_workspace_size(B,H,Hkv,Nq,d) bytes
+ *                 of device scratch, contents on entry ignored; not to be used
+ *                 by another call that overlaps this one on the GPU
+ * A row that sees no key (length 0, or causal with i < Nq - seq_lens[b]) gets
+ * O = 0 and LSE = -inf.  Bytes of the cache at or behind a request's length
+ * have no effect, whatever they are.  A key or query with a NaN makes the rows
+ * that see it NaN.  The scales that count must be finite, 0 or within
+ * 2^-60..2^60 in size.
+ */
+FA_API fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                         const float* k_scale, const float* v_scale, const int* block_table,
+                                         const int* seq_lens, void* o, float* lse, int B, int H, int Hkv, int Nq,
+                                         int d, int num_pages, int page_size, int max_pages, float scale, int causal,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace fa_fwd_decode_paged_fp8 needs ((size_t)-1 for invalid arguments). */
+FA_API size_t fa_fwd_decode_paged_fp8_workspace_size(int B, int H, int Hkv, int Nq, int d);
+
 /* Human-readable text for a status code (static storage, never NULL). */
 FA_API const char* fa_strerror(fa_status status);
 
@@ -293,8 +434,9 @@ FA_API const char* fa_strerror(fa_status status);
  * Reads and clears the library's device status word on the current device.
  * Synchronises `stream` first.  Returns FA_OK, or FA_ERR_DEVICE_TIMEOUT if a
  * bounded wait inside a kernel ran out since the last call (the kernel then
- * abandoned its tile and returned; its outputs are undefined).  *where, if
- * not NULL, receives a code naming the wait that gave up.
+ * abandoned its tile and returned; its outputs are undefined), or
+ * FA_ERR_BAD_PAGE if a kernel skipped a page or slot outside the cache.
+ * *where, if not NULL, receives a code naming the wait or the check.
  */
 FA_API fa_status fa_device_status(void* stream, uint32_t* where);
 
