@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_paged_simple(const PagedAr
         report_status(a.status, DEVSTATUS_BAD_PAGE, WAIT_PAGED_TABLE);
       }
     }
-    float mt = s;
+    float mt = s == s ? s : 0.0f;      // a NaN score must not hide from the maximum: its p is NaN
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
     const float mn = fmaxf(m, mt);
