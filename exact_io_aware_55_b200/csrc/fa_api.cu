@@ -598,6 +598,41 @@ bool cache_fits(int num_pages, int Hkv, int page_size) {
          static_cast<long long>(num_pages) * page_size <= 0x7fffffffll;
 }
 
+// Paged decode: query rows that share a KV head go in tiles of 8, 16 or 32 (the
+// smallest that holds them; a row costs an exponential per key, used or not).
+// One CTA per SM (148 assumed, so that the workspace size needs no device
+// query) with two slots for pieces and a note each.
+struct PagedPlan {
+  int row_tile, row_tiles;
+  size_t lse_off, notes_off, total;
+};
+PagedPlan paged_plan(int H, int Hkv, int Nq, int d) {
+  PagedPlan p{};
+  const int rows = H / Hkv * Nq;
+  p.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
+  const size_t parts = size_t(2) * kDecodePlanSMs * p.row_tile;
+  p.lse_off = parts * d * 4;
+  p.notes_off = p.lse_off + parts * 4;
+  p.total = p.notes_off + kDecodePlanSMs * sizeof(fa::PagedNote);
+  return p;
+}
+
+// 3-D tensor map over the codes of a paged cache [pages * heads, page, d], box
+// one page of one head, swizzled over the d bytes of a row.
+bool make_map_pages(CUtensorMap* map, const void* base, int d, int page, int rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(page), cuuint64_t(rows)};
+  cuuint64_t strides[2] = {cuuint64_t(d), cuuint64_t(page) * d};
+  cuuint32_t box[3] = {cuuint32_t(d), cuuint32_t(page), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 fa_status check_paged(int B, int H, int Hkv, int Nq, int d, float scale, int causal, bool* empty) {
   if (B < 0 || H < 0 || Hkv < 0 || Nq < 0) return FA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
@@ -749,7 +784,8 @@ fa_status fa_cache_append_fp8(const void* k, const void* v, const int* slots, vo
 size_t fa_fwd_decode_paged_fp8_workspace_size(int B, int H, int Hkv, int Nq, int d) {
   bool empty = false;
   if (check_paged(B, H, Hkv, Nq, d, 1.0f, 0, &empty) != FA_OK) return static_cast<size_t>(-1);
-  return 0;
+  if (empty) return 0;
+  return paged_plan(H, Hkv, Nq, d).total;
 }
 
 fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -768,8 +804,11 @@ fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void
   if (!q || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
   if ((max_pages > 0 && !block_table) || (num_pages > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)))
     return FA_ERR_INVALID_ARG;
-  const size_t need = fa_fwd_decode_paged_fp8_workspace_size(B, H, Hkv, Nq, d);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+  const PagedPlan plan = paged_plan(H, Hkv, Nq, d);
+  // the tiles of one request are counted in 32 bits
+  if ((static_cast<long long>(max_pages) * page_size / 128 + 1) * Hkv * plan.row_tiles > 0x7fffffffll)
+    return FA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < plan.total) return FA_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
       !aligned(workspace, 16))
@@ -779,24 +818,33 @@ fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void
   fa::PagedArgs a{};
   a.status = status;
   a.q = q;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.block_table = block_table;
   a.seq_lens = seq_lens;
   a.o = o;
   a.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + plan.lse_off);
+  a.notes = reinterpret_cast<fa::PagedNote*>(ws + plan.notes_off);
   a.B = B;
-  a.H = H;
   a.Hkv = Hkv;
   a.Nq = Nq;
+  a.rows = H / Hkv * Nq;
+  a.row_tiles = plan.row_tiles;
+  a.units = Hkv * plan.row_tiles;
   a.num_pages = num_pages;
   a.page = page_size;
-  a.max_pages = num_pages > 0 ? max_pages : 0;
+  a.max_pages = num_pages > 0 ? max_pages : 0;    // without pages every request is empty
   a.causal = causal;
   a.c_log2 = scale * kLog2e;
-  return launch_status(fa::launch_decode_paged(a, d, static_cast<cudaStream_t>(stream)));
+  CUtensorMap tk{}, tv{};
+  if (a.max_pages > 0 && (!make_map_pages(&tk, k_cache, d, page_size, num_pages * Hkv) ||
+                          !make_map_pages(&tv, v_cache, d, page_size, num_pages * Hkv)))
+    return FA_ERR_LAUNCH;
+  return launch_status(fa::launch_decode_paged(tk, tv, a, d, plan.row_tile, kDecodePlanSMs,
+                                               static_cast<cudaStream_t>(stream)));
 }
 
 const char* fa_strerror(fa_status s) {

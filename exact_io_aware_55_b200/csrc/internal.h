@@ -59,10 +59,23 @@ enum WaitSite : uint32_t {
   WAIT_STD_PV_EMPTY = 66,
   WAIT_STD_PV_FULL = 67,
   WAIT_STD_PV_DONE = 68,
+  WAIT_PAGED_Q = 70,
+  WAIT_PAGED_Q_EMPTY = 71,
+  WAIT_PAGED_KV = 72,
+  WAIT_PAGED_KV_EMPTY = 73,
+  WAIT_PAGED_SC_EMPTY = 74,
+  WAIT_PAGED_S = 75,
+  WAIT_PAGED_S_FREE = 76,
+  WAIT_PAGED_P = 77,
+  WAIT_PAGED_PV = 78,
+  WAIT_PAGED_RED = 79,
   // sites that report a page or slot outside the cache
   WAIT_APPEND_SLOT = 80,
   WAIT_TABLES_BACK = 81,
   WAIT_PAGED_TABLE = 82,
+  WAIT_PAGED_O = 83,
+  WAIT_PAGED_O_FREE = 84,
+  WAIT_PAGED_STATS = 85,
   WAIT_SELFTEST = 99,
 };
 
@@ -231,23 +244,32 @@ struct TableArgs {
 cudaError_t launch_page_tables(const TableArgs& a, cudaStream_t stream);
 
 // Attention over the 8-bit paged cache (fa_decode_paged.cu).
+struct PagedNote {     // a CTA ended unit (b, unit), which CTA `first` began (b < 0: it ended none that it did not begin)
+  int b, unit, first, pad;
+};
 struct PagedArgs {
   uint32_t* status;
   const void* q;            // bf16 [B, H, Nq, d]
-  const void* k_cache;      // e4m3 [num_pages, Hkv, page, d]
-  const void* v_cache;
   const float* k_scale;     // [num_pages, Hkv]
   const float* v_scale;
   const int* block_table;   // [B, max_pages]
   const int* seq_lens;      // [B]
   void* o;                  // bf16 [B, H, Nq, d]
   float* lse;               // [B, H, Nq]
-  int B, H, Hkv, Nq;
+  float* part_o;            // workspace: fp32 [2 * CTAs, row tile, d], pieces of units cut between CTAs
+  float* part_lse;          // workspace: fp32 [2 * CTAs, row tile]
+  PagedNote* notes;         // workspace: [CTAs]
+  int B, Hkv, Nq;
+  int rows;                 // query rows that share a KV head: H / Hkv * Nq
+  int row_tiles;            // tiles of them
+  int units;                // Hkv * row_tiles
   int num_pages, page, max_pages;
   int causal;
   float c_log2;             // scale * log2(e)
 };
-cudaError_t launch_decode_paged(const PagedArgs& a, int d, cudaStream_t stream);
+// tk, tv: maps over the codes as [num_pages * Hkv, page, d], box one page, swizzled over d bytes.
+cudaError_t launch_decode_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int d, int row_tile,
+                                int ctas, cudaStream_t stream);
 
 cudaError_t launch_watchdog_selftest(uint64_t limit_ns, cudaStream_t stream);
 
