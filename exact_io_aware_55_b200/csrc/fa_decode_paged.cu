@@ -38,8 +38,8 @@
 // results do not depend on timing.
 //
 // Warps: 0 page ids and TMA, 1 MMA issuer and TMEM owner, 2 page scales,
-// 3 queries, 4-7 softmax (thread = key; TMEM lane quarter = warp % 4),
-// 8-11 epilogue.  Pages that lie behind the length or outside the cache are not
+// 3 queries, 4-7 and 8-11 softmax (thread = key, each group half of the rows;
+// TMEM lane quarter = warp % 4), 12-15 epilogue.  Pages that lie behind the length or outside the cache are not
 // loaded; the softmax warps clear the V rows of keys that are not there, since
 // p = 0 times a stale NaN code would be NaN.
 #include <cuda_bf16.h>
@@ -53,18 +53,18 @@ namespace fa {
 
 namespace {
 
-constexpr int kPgThreads = 384;
+constexpr int kPgThreads = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
 constexpr float kBase = 2048.0f;            // P is scaled by 2^11: at most 2^15, of e5m2's 57344
 
 template <int D, int R>
 struct PgShape {
-  static constexpr int kSub = (D == 64 && R <= 16) ? 2 : 1;   // 128-key sub-tiles per tile
+  static constexpr int kSub = (D == 64) ? 2 : 1;              // 128-key sub-tiles per tile
   static constexpr int kTileKeys = 128 * kSub;
   static constexpr int kTileBytes = kTileKeys * D;            // K (or V) codes of one tile
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kNS = (R == 32) ? (D == 64 ? 10 : 5) : 6;   // ring depth: 160 or 192 KB
+  static constexpr int kNS = (R == 32) ? 5 : 6;               // ring depth: 160 or 192 KB
   static constexpr int kMaxPages = kTileKeys / 16;
   static constexpr int kQRows = 2 * R;                        // hi, lo
   static constexpr int kQBytes = kQRows * D;
@@ -88,12 +88,11 @@ struct PgBarriers {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2], pv_done[2];
-  uint64_t red[2];
   uint64_t o_full[2], o_free[2];
   uint64_t stats_full[2];
   alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, log2 vs, 1 / vs, share of vs
   alignas(16) float q_factor[2][R];        // power of two that a row of queries was divided by
-  alignas(16) float red_max[2][4][R];      // per-warp tile maxima (log2 units)
+  alignas(16) float red_max[4][R];         // per-warp tile maxima (log2 units)
   alignas(16) float stat_m[2][R];          // piece's running max
   alignas(16) float stat_l[2][4][R];       // piece's per-warp sums
   long long scan[kPgThreads / 32];
@@ -129,6 +128,71 @@ __device__ __forceinline__ float redux_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
+}
+// Hardware barrier of the 128 threads of a softmax group, and one that also
+// tells whether `x` holds for any of them.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "memory");
+  return y != 0;
+}
+// Two warp-uniform waits whose first looks overlap.
+__device__ __forceinline__ bool mbar_wait2_warp(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, const WaitCtx& w,
+                                                uint32_t where) {
+  const bool a = mbar_try_wait(x, px), b = mbar_try_wait(y, py);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return mbar_wait_warp(x, px, w, where) && mbar_wait_warp(y, py, w, where);
+}
+
+// N (4, 8, 16) consecutive TMEM columns of this thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[N]) {
+  if constexpr (N == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(t) : "memory");
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t) : "memory");
+  else
+    tmem_ld_x16(t, r);
+}
+// Two such loads with one wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld2(uint32_t t, uint32_t t2, uint32_t (&r)[N], uint32_t (&q)[N]) {
+  if constexpr (N == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%8];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%9];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+                 : "r"(t), "r"(t2) : "memory");
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7])
+                 : "r"(t), "r"(t2) : "memory");
+  else {
+    tmem_ld_x16(t, r);
+    tmem_ld_x16(t2, q);
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[N]) {
+  if constexpr (N == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]) : "memory");
+  else if constexpr (N == 8)
+    tmem_st_x8(t, r);
+  else
+    tmem_st_x16(t, r);
 }
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -233,15 +297,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b->q_full[i], 1);
-      mbar_init(&b->q_empty[i], 5);
+      mbar_init(&b->q_empty[i], 9);
       mbar_init(&b->s_full[i], 1);
-      mbar_init(&b->s_free[i], 4);
-      mbar_init(&b->p_full[i], 4);
+      mbar_init(&b->s_free[i], 8);
+      mbar_init(&b->p_full[i], 8);
       mbar_init(&b->pv_done[i], 1);
-      mbar_init(&b->red[i], 4);
       mbar_init(&b->o_full[i], 1);
       mbar_init(&b->o_free[i], 4);
-      mbar_init(&b->stats_full[i], 4);
+      mbar_init(&b->stats_full[i], 8);
     }
     b->abort = 0u;
     fence_mbar_init();
@@ -477,61 +540,51 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->q_full[qb]);
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ------------------------------------------------------------- softmax
+    // Two groups of four warps; each has half of the rows, for every key.
+    constexpr int H = R / 2;
     const int wq = warp & 3;
+    const int half = (warp >> 2) - 1;
+    const int hr = half * H;                         // this group's first row
     const uint32_t lane_base = tmem + (uint32_t(wq * 32) << 16);
     const int page_shift = 31 - __clz(a.page);
     Walk<TILE> walk(a, g0, g1, b0, base0);
     Piece pc;
+    // A warp whose wait ran out goes on without waiting or arriving, so that
+    // the group's hardware barriers are still met by all four warps.
     bool ok = true;
     int g = 0, it = 0;
-    for (; ok && walk.next(pc); ++it) {
+    for (; walk.next(pc); ++it) {
       const int ob = it & 1, qb = it & 1;
-      const int row0 = (pc.unit % a.row_tiles) * R;
-      float m_used[R], l_t[R];
+      const int row0 = (pc.unit % a.row_tiles) * R + hr;
+      float m_used[H], l_t[H];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < H; ++r) {
         m_used[r] = -INFINITY;
         l_t[r] = 0.0f;
       }
       // the queries' factors are this warp's to read from here on
-      if (!mbar_wait_warp(&b->q_full[qb], (it >> 1) & 1, wc, WAIT_PAGED_Q)) break;
+      ok = ok && mbar_wait_warp(&b->q_full[qb], (it >> 1) & 1, wc, WAIT_PAGED_Q);
       for (int j = 0; j < pc.n; ++j, ++g) {
         const int sb = g & 1, st = g % NS;
-        if (!mbar_wait_warp(&b->kv_full[st], (g / NS) & 1, wc, WAIT_PAGED_KV) ||
-            !mbar_wait_warp(&b->s_full[sb], (g >> 1) & 1, wc, WAIT_PAGED_S)) {
-          ok = false;
-          break;
-        }
+        ok = ok && mbar_wait2_warp(&b->kv_full[st], (g / NS) & 1, &b->s_full[sb], (g >> 1) & 1, wc, WAIT_PAGED_S);
         tc_fence_after();
         const int tile0 = (pc.j0 + j) * TILE;
-        float s[U][R];
+        float s[U][H];
         float inv[U], share[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const uint32_t col = lane_base + S::kColS + S::kQRows * (sb * U + u);
-          if constexpr (R == 8) {
-            uint32_t x[16];
-            tmem_ld_x16(col, x);
+          const uint32_t col = lane_base + S::kColS + S::kQRows * (sb * U + u) + hr;
+          uint32_t x[H], y[H];
+          tmem_ld2<H>(col, col + R, x, y);
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-              s[u][r] = fmaf(__uint_as_float(x[8 + r]), 0.0625f, __uint_as_float(x[r]));
-          } else {
-#pragma unroll
-            for (int rg = 0; rg < R; rg += 16) {
-              uint32_t x[16], y[16];
-              tmem_ld_x16(col + rg, x);
-              tmem_ld_x16(col + R + rg, y);
-#pragma unroll
-              for (int r = 0; r < 16; ++r)
-                s[u][rg + r] = fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r]));
-            }
-          }
+          for (int r = 0; r < H; ++r) s[u][r] = fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r]));
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->s_free[sb]);
+        if (ok && lane == 0) mbar_arrive(&b->s_free[sb]);
+        bool need = false;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int kt = 128 * u + wq * 32 + lane;
@@ -540,105 +593,84 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           share[u] = f.w;
           const bool there = tile0 + kt < pc.len && f.y != -INFINITY;
 #pragma unroll
-          for (int r = 0; r < R; r += 4) {
-            const float4 qf = *reinterpret_cast<const float4*>(&b->q_factor[qb][r]);
+          for (int r = 0; r < H; r += 4) {
+            const float4 qf = *reinterpret_cast<const float4*>(&b->q_factor[qb][hr + r]);
             s[u][r] = there ? fmaf(s[u][r], qf.x * f.x, f.y) : -INFINITY;
             s[u][r + 1] = there ? fmaf(s[u][r + 1], qf.y * f.x, f.y) : -INFINITY;
             s[u][r + 2] = there ? fmaf(s[u][r + 2], qf.z * f.x, f.y) : -INFINITY;
             s[u][r + 3] = there ? fmaf(s[u][r + 3], qf.w * f.x, f.y) : -INFINITY;
           }
-          if (!there) {      // stale codes of V must not meet p = 0
-            uint8_t* v = sKV + st * S::kStageBytes + S::kTileBytes + kt * D;
+          if (!there) {      // stale codes of V must not meet p = 0; each group clears half of the row
+            uint8_t* v = sKV + st * S::kStageBytes + S::kTileBytes + kt * D + half * (D / 2);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         if (a.causal && tile0 + TILE > pc.len - a.Nq + 1) {
           int i = row0 % a.Nq;                       // query of row r
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
+          for (int r = 0; r < H; ++r) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
               if (tile0 + 128 * u + wq * 32 + lane > pc.len - a.Nq + i) s[u][r] = -INFINITY;
             i = i + 1 == a.Nq ? 0 : i + 1;
           }
         }
-        // tile maximum per row: warp redux, then the four softmax warps
-        float* rm = &b->red_max[sb][wq][0];
+        // Does any key of the tile lift a row's maximum by more than the
+        // threshold?  One barrier with a vote; the maxima themselves are only
+        // exchanged when one does.
 #pragma unroll
-        for (int r = 0; r < R; r += 4) {
-          float x[4];
+        for (int r = 0; r < H; ++r)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[k] = s[0][r + k];
+          for (int u = 0; u < U; ++u) need |= s[u][r] > m_used[r] + kRescaleThreshold;
+        if (group_any(1 + half, need)) {
 #pragma unroll
-            for (int u = 1; u < U; ++u) x[k] = fmaxf(x[k], s[u][r + k]);
-            x[k] = redux_max(x[k]);
+          for (int r = 0; r < H; ++r) {
+            float x = s[0][r];
+#pragma unroll
+            for (int u = 1; u < U; ++u) x = fmaxf(x, s[u][r]);
+            x = redux_max(x);
+            if (lane == 0) b->red_max[wq][hr + r] = x;
           }
-          if (lane == 0) *reinterpret_cast<float4*>(rm + r) = make_float4(x[0], x[1], x[2], x[3]);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b->red[sb]);
-        if (!mbar_wait_warp(&b->red[sb], (g >> 1) & 1, wc, WAIT_PAGED_RED)) {
-          ok = false;
-          break;
-        }
-        // The maxima are read twice (once to see whether any row has to move)
-        // to keep them out of registers.
-        bool need = false;
+          group_sync(1 + half);
+          float alpha[H];
 #pragma unroll
-        for (int r = 0; r < R; r += 4) {
-          const float4 x0 = *reinterpret_cast<const float4*>(&b->red_max[sb][0][r]);
-          const float4 x1 = *reinterpret_cast<const float4*>(&b->red_max[sb][1][r]);
-          const float4 x2 = *reinterpret_cast<const float4*>(&b->red_max[sb][2][r]);
-          const float4 x3 = *reinterpret_cast<const float4*>(&b->red_max[sb][3][r]);
-          need |= fmaxf(fmaxf(x0.x, x1.x), fmaxf(x2.x, x3.x)) > m_used[r] + kRescaleThreshold;
-          need |= fmaxf(fmaxf(x0.y, x1.y), fmaxf(x2.y, x3.y)) > m_used[r + 1] + kRescaleThreshold;
-          need |= fmaxf(fmaxf(x0.z, x1.z), fmaxf(x2.z, x3.z)) > m_used[r + 2] + kRescaleThreshold;
-          need |= fmaxf(fmaxf(x0.w, x1.w), fmaxf(x2.w, x3.w)) > m_used[r + 3] + kRescaleThreshold;
-        }
-        if (need) {   // uniform: every thread holds the same m_used and maxima
-          float alpha[R];
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float mt = fmaxf(fmaxf(b->red_max[sb][0][r], b->red_max[sb][1][r]),
-                                   fmaxf(b->red_max[sb][2][r], b->red_max[sb][3][r]));
+          for (int r = 0; r < H; ++r) {
+            const float mt = fmaxf(fmaxf(b->red_max[0][hr + r], b->red_max[1][hr + r]),
+                                   fmaxf(b->red_max[2][hr + r], b->red_max[3][hr + r]));
             const float mn = fmaxf(m_used[r], mt);
             alpha[r] = (mn == -INFINITY) ? 1.0f : ex2_approx(m_used[r] - mn);
             m_used[r] = mn;
             l_t[r] *= alpha[r];
           }
           if (j > 0) {   // O^T holds earlier tiles of this piece: rescale it once PV(g-1) is done
-            if (!mbar_wait_warp(&b->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_PV)) {
-              ok = false;
-              break;
-            }
+            ok = ok && mbar_wait_warp(&b->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_PV);
             tc_fence_after();
+            if (ok) {
 #pragma unroll
-            for (int c = 0; c < (R == 8 ? 32 : 3 * R); c += 16) {
-              uint32_t o[16];
-              tmem_ld_x16(lane_base + S::kColO + S::kPRows * ob + c, o);
+              for (int part = 0; part < 3; ++part) {
+                const uint32_t col = lane_base + S::kColO + S::kPRows * ob + part * R + hr;
+                uint32_t o[H];
+                tmem_ld<H>(col, o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha[(c + k) % R]);
-              tmem_st_x16(lane_base + S::kColO + S::kPRows * ob + c, o);
+                for (int r = 0; r < H; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
+                tmem_st<H>(col, o);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
           }
         }
         // P^T into shared memory: B operand, K-major, rows = parts of the query
-        // rows, the sub-tile's 128 keys in one 128-byte swizzled row.
+        // rows, the sub-tile's 128 keys in one 128-byte swizzled row.  The
+        // buffer is free: S(g) was committed behind PV(g - 2), which read it.
         const int pb = g & 1;
-        if (g >= 2 && !mbar_wait_warp(&b->pv_done[pb], ((g - 2) >> 1) & 1, wc, WAIT_PAGED_PV)) {
-          ok = false;
-          break;
-        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int key = wq * 32 + lane;
-          uint8_t* pbase = sP + pb * S::kPBytes + u * S::kPSub + (key & 15);
+          uint8_t* pbase = sP + pb * S::kPBytes + u * S::kPSub + (key & 15) + hr * 128;
           const int unit = key >> 4;
 #pragma unroll
-          for (int r = 0; r < R; r += 2) {
+          for (int r = 0; r < H; r += 2) {
             const float p0 = (s[u][r] == -INFINITY) ? 0.0f : ex2_approx(s[u][r] - m_used[r]);
             const float p1 = (s[u][r + 1] == -INFINITY) ? 0.0f : ex2_approx(s[u][r + 1] - m_used[r + 1]);
             l_t[r] = fmaf(p0, inv[u], l_t[r]);
@@ -651,8 +683,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             const uint32_t mid = (*reinterpret_cast<const uint32_t*>(&d1) + 0x00800080u) & 0xff00ff00u;
             const __half2 d2 = __hmul2(__hsub2(d1, *reinterpret_cast<const __half2*>(&mid)), __float2half2_rn(8.0f));
             const uint32_t lo = *reinterpret_cast<const uint32_t*>(&d2) + 0x00800080u;
-            uint8_t* p_even = pbase + r * 128 + ((unit ^ (r & 7)) << 4);
-            uint8_t* p_odd = pbase + (r + 1) * 128 + ((unit ^ ((r + 1) & 7)) << 4);
+            // hr is 4 or a multiple of 8: row & 7 as the swizzle sees it
+            const int x0 = ((H == 4 ? hr : 0) + r) & 7;
+            uint8_t* p_even = pbase + r * 128 + ((unit ^ x0) << 4);
+            uint8_t* p_odd = pbase + (r + 1) * 128 + ((unit ^ (x0 + 1)) << 4);
             p_even[0] = static_cast<uint8_t>(hi >> 8);
             p_odd[0] = static_cast<uint8_t>(hi >> 24);
             p_even[R * 128] = static_cast<uint8_t>(mid >> 8);
@@ -664,24 +698,23 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->p_full[pb]);
+        if (ok && lane == 0) mbar_arrive(&b->p_full[pb]);
       }
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(&b->q_empty[qb]);
+      if (ok && lane == 0) mbar_arrive(&b->q_empty[qb]);
       // Piece done: once its last PV has completed (which also orders these
       // writes after the epilogue's read of this stats buffer two pieces ago),
       // publish the running max and the per-warp sums.
-      if (!mbar_wait_warp(&b->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_PV)) break;
+      ok = ok && mbar_wait_warp(&b->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_PV);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < H; ++r) {
         const float l = warp_sum(l_t[r]);
-        if (lane == 0) {
-          b->stat_l[ob][wq][r] = l;
-          if (wq == 0) b->stat_m[ob][r] = m_used[r];
+        if (ok && lane == 0) {
+          b->stat_l[ob][wq][hr + r] = l;
+          if (wq == 0) b->stat_m[ob][hr + r] = m_used[r];
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b->stats_full[ob]);
+      if (ok && lane == 0) mbar_arrive(&b->stats_full[ob]);
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -754,12 +787,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->o_free[ob]);
     }
-    if (threadIdx.x == 256) a.notes[blockIdx.x] = note;
+    if (threadIdx.x == 384) a.notes[blockIdx.x] = note;
   }
-  if (n_tiles == 0 && threadIdx.x == 256) a.notes[blockIdx.x] = PagedNote{-1, 0, 0, 0};
+  if (n_tiles == 0 && threadIdx.x == 384) a.notes[blockIdx.x] = PagedNote{-1, 0, 0, 0};
   // requests without a token
-  if (warp >= 8) {
-    const int t = threadIdx.x - 256;
+  if (warp >= 12) {
+    const int t = threadIdx.x - 384;
     for (int i = blockIdx.x; i < a.B; i += gridDim.x) {
       if (pg_len(a, i) > 0) continue;
       const size_t rows = static_cast<size_t>(a.Hkv) * a.rows;

@@ -68,7 +68,6 @@ enum WaitSite : uint32_t {
   WAIT_PAGED_S_FREE = 76,
   WAIT_PAGED_P = 77,
   WAIT_PAGED_PV = 78,
-  WAIT_PAGED_RED = 79,
   // sites that report a page or slot outside the cache
   WAIT_APPEND_SLOT = 80,
   WAIT_TABLES_BACK = 81,
