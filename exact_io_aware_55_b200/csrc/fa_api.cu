@@ -600,8 +600,7 @@ bool cache_fits(int num_pages, int Hkv, int page_size) {
 
 // Paged decode: query rows that share a KV head go in tiles of 8, 16 or 32 (the
 // smallest that holds them; a row costs an exponential per key, used or not).
-// One CTA per SM (148 assumed, so that the workspace size needs no device
-// query) with two slots for pieces and a note each.
+// kPagedCtas CTAs with two slots for pieces and a note each.
 struct PagedPlan {
   int row_tile, row_tiles;
   size_t lse_off, notes_off, total;
@@ -611,10 +610,10 @@ PagedPlan paged_plan(int H, int Hkv, int Nq, int d) {
   const int rows = H / Hkv * Nq;
   p.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
-  const size_t parts = size_t(2) * kDecodePlanSMs * p.row_tile;
+  const size_t parts = size_t(2) * fa::kPagedCtas * p.row_tile;
   p.lse_off = parts * d * 4;
   p.notes_off = p.lse_off + parts * 4;
-  p.total = p.notes_off + kDecodePlanSMs * sizeof(fa::PagedNote);
+  p.total = p.notes_off + fa::kPagedCtas * sizeof(fa::PagedNote);
   return p;
 }
 
@@ -805,8 +804,8 @@ fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void
   if ((max_pages > 0 && !block_table) || (num_pages > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)))
     return FA_ERR_INVALID_ARG;
   const PagedPlan plan = paged_plan(H, Hkv, Nq, d);
-  // the tiles of one request are counted in 32 bits
-  if ((static_cast<long long>(max_pages) * page_size / 128 + 1) * Hkv * plan.row_tiles > 0x7fffffffll)
+  // the tiles of one request, and one head's tiles of all, are counted in 32 bits
+  if (static_cast<long long>(B) * max_pages > 0x7fffffffll || (static_cast<long long>(max_pages) * page_size / 128 + 1) * Hkv * plan.row_tiles > 0x7fffffffll)
     return FA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < plan.total) return FA_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
@@ -843,8 +842,8 @@ fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void
   if (a.max_pages > 0 && (!make_map_pages(&tk, k_cache, d, page_size, num_pages * Hkv) ||
                           !make_map_pages(&tv, v_cache, d, page_size, num_pages * Hkv)))
     return FA_ERR_LAUNCH;
-  return launch_status(fa::launch_decode_paged(tk, tv, a, d, plan.row_tile, kDecodePlanSMs,
-                                               static_cast<cudaStream_t>(stream)));
+  return launch_status(
+      fa::launch_decode_paged(tk, tv, a, d, plan.row_tile, static_cast<cudaStream_t>(stream)));
 }
 
 const char* fa_strerror(fa_status s) {

@@ -19,12 +19,13 @@
 //   O^T += V^T P^T  d x rows (A = V tile, MN-major).  p * vs is rounded to fp16
 //                   and split into three e5m2 parts, hi + mid/8 + lo/64, which
 //                   is exact: 11 bits in three times 3 plus the signs.  e5m2 has
-//                   fp16's exponent range, so a key down to 2^-29 of the largest
+//                   fp16's exponent range, so a key down to 2^-28 of the largest
 //                   keeps its 11 bits.  A and B of one product may differ in
 //                   type among the 8-bit floats.
-// A page's K scale multiplies its keys' scores; its V scale is added to the
-// score's exponent (t = s + log2 vs, P = exp2(t - m)), so that the parts cannot
-// overflow whatever the scales are, and l sums exp2(t - m) / vs.
+// A page's K scale multiplies its keys' scores; the power of two in its V scale
+// is added to the score's exponent (t = s + e, P = exp2(t - m) * vs / 2^e), so
+// that the parts cannot overflow whatever the scales are, and l sums
+// exp2(t - m) / 2^e.
 //
 // Work.  A unit is (request, KV head, tile of up to R query rows); its keys are
 // cut into tiles of 128 (d = 128) or 256 (d = 64) tokens, 32 KB of codes.  The
@@ -54,9 +55,9 @@ namespace fa {
 namespace {
 
 constexpr int kPgThreads = 512;
-constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
-constexpr float kBase = 2048.0f;            // P is scaled by 2^11: at most 2^15, of e5m2's 57344
+constexpr float kBase = 1024.0f;            // P is scaled by 2^10: below 2^15, of e5m2's 57344
 
 template <int D, int R>
 struct PgShape {
@@ -82,6 +83,11 @@ struct PgShape {
   static_assert(kCols <= 512, "TMEM columns");
 };
 
+// A place among the tiles: tile j of unit `unit` of request b, which has nt.
+struct Place {
+  int b, unit, j, len, nt;
+};
+
 template <int R, int NS, int PAGES>
 struct PgBarriers {
   uint64_t kv_full[NS], kv_empty[NS];
@@ -90,14 +96,14 @@ struct PgBarriers {
   uint64_t p_full[2], pv_done[2];
   uint64_t o_full[2], o_free[2];
   uint64_t stats_full[2];
-  alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, log2 vs, 1 / vs, share of vs
+  alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, e, 2^-e, vs / 2^e
   alignas(16) float q_factor[2][R];        // power of two that a row of queries was divided by
   alignas(16) float red_max[4][R];         // per-warp tile maxima (log2 units)
   alignas(16) float stat_m[2][R];          // piece's running max
   alignas(16) float stat_l[2][4][R];       // piece's per-warp sums
-  long long scan[kPgThreads / 32];
-  long long start_base;
-  int start_b;
+  uint32_t nan_keys[2][128];               // per column of a piece: boundary keys whose V code is NaN
+  alignas(16) unsigned scan[kPgThreads / 32];
+  Place start;
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -142,13 +148,26 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
       : "memory");
   return y != 0;
 }
-// Two warp-uniform waits whose first looks overlap.
-__device__ __forceinline__ bool mbar_wait2_warp(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, const WaitCtx& w,
-                                                uint32_t where) {
-  const bool a = mbar_try_wait(x, px), b = mbar_try_wait(y, py);
-  if (__all_sync(0xffffffffu, a && b)) return true;
-  return mbar_wait_warp(x, px, w, where) && mbar_wait_warp(y, py, w, where);
+// Bounded waits.  The roles' code shares the SM's instruction cache, so only
+// the first look is inline.
+__device__ __noinline__ bool pg_wait_slow(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, w, where));
 }
+__device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t where) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || pg_wait_slow(bar, parity, w, where);
+}
+// Three waits whose first looks overlap.
+__device__ __forceinline__ bool pg_wait3(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, uint64_t* z, uint32_t pz,
+                                         const WaitCtx& w, uint32_t where) {
+  const bool a = mbar_try_wait(x, px), b = mbar_try_wait(y, py), c = mbar_try_wait(z, pz);
+  return __all_sync(0xffffffffu, a && b && c) ||
+         (pg_wait_slow(x, px, w, where) && pg_wait_slow(y, py, w, where) && pg_wait_slow(z, pz, w, where));
+}
+
+// Programmatic dependent launch: wait for the grids before this one in the
+// stream, and let the one behind it be set up.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // N (4, 8, 16) consecutive TMEM columns of this thread's lane.
 template <int N>
@@ -200,76 +219,111 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
+// Two bf16 queries times `inv` (below 256) as two e4m3 parts each: the value
+// rounded, and 16 times what is left of it.
+__device__ __forceinline__ void split_pair(uint32_t q, float inv, uint32_t& hi, uint32_t& lo) {
+  const float x = __uint_as_float(q << 16) * inv, y = __uint_as_float(q & 0xffff0000u) * inv;
+  hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  lo = __nv_cvt_float2_to_fp8x2(make_float2((x - f.x) * 16.0f, (y - f.y) * 16.0f), __NV_SATFINITE, __NV_E4M3);
+}
+
 __device__ __forceinline__ int pg_len(const PagedArgs& a, int b) { return min(max(a.seq_lens[b], 0), a.max_pages * a.page); }
+
+// Clears the NaN codes (0x7f, 0xff) in one half of row `kt` of a V tile and sets
+// bit `edge` for their columns; the flags of the piece two before are the
+// epilogue's until it frees them.
+template <int D>
+__device__ __noinline__ bool clear_nan_codes(uint8_t* v, int kt, int half, int edge, uint32_t* nan_keys,
+                                             uint64_t* o_free, int it, bool ok, const WaitCtx& wc) {
+  uint32_t* row = reinterpret_cast<uint32_t*>(v + kt * D + half * (D / 2));
+  bool waited = it < 2;
+  for (int c = 0; c < D / 8; ++c) {
+    const uint32_t x = row[c], bad = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    if (bad == 0u) continue;
+    if (!waited) ok = ok && mbar_wait(o_free, ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE);
+    waited = true;
+    row[c] = x & ~bad;
+    const int byte = half * (D / 2) + c * 4;                       // place in the swizzled row
+    const int unit = (byte >> 4) ^ (D == 128 ? kt & 7 : (kt >> 1) & 3);
+    for (int k = 0; k < 4; ++k)
+      if ((bad >> (8 * k)) & 1u) atomicOr(&nan_keys[unit * 16 + (byte & 15) + k], 1u << edge);
+  }
+  return ok;
+}
+
+__device__ __forceinline__ int kv_head(const PagedArgs& a, int unit) { return a.row_tiles == 1 ? unit : unit / a.row_tiles; }
 
 // A piece: tiles [j0, j0 + n) of one unit.
 struct Piece {
   int b, unit, len, nt, j0, n;
 };
-// Walks over a CTA's range of tiles, piece by piece.
+// Walks over a CTA's range of tiles; `left` are to come.
 template <int TILE>
 struct Walk {
   const PagedArgs& a;
-  long long g, g1, base;      // next tile, end of the range, first tile of request b
-  int b, len, nt;
-  __device__ __forceinline__ Walk(const PagedArgs& a_, long long g0, long long g1_, int b0, long long base0)
-      : a(a_), g(g0), g1(g1_), base(base0), b(b0), len(0), nt(0) {
-    if (g < g1) load();
-  }
-  __device__ __forceinline__ void load() {
-    len = pg_len(a, b);
-    nt = (len + TILE - 1) / TILE;
-  }
-  // Unit and tile of position `at` (>= g of the last call).
-  __device__ __forceinline__ void seek(long long at, int& unit, int& j) {
-    while (at >= base + static_cast<long long>(nt) * a.units) {
-      base += static_cast<long long>(nt) * a.units;
-      ++b;
-      load();
+  Place p;
+  int left;
+  __device__ __forceinline__ Walk(const PagedArgs& a_, const Place& start, int n) : a(a_), p(start), left(n) {}
+  // Carries tile counts over a unit's end into the next units.
+  __device__ __forceinline__ void settle() {
+    while (p.j >= p.nt) {
+      p.j -= p.nt;
+      if (++p.unit == a.units) {
+        p.unit = 0;
+        do {
+          p.len = pg_len(a, ++p.b);
+          p.nt = (p.len + TILE - 1) / TILE;
+        } while (p.nt == 0);
+      }
     }
-    const int local = static_cast<int>(at - base);
-    unit = local / nt;
-    j = local - unit * nt;
   }
-  __device__ __forceinline__ bool next(Piece& p) {
-    if (g >= g1) return false;
-    seek(g, p.unit, p.j0);
-    p.b = b;
-    p.len = len;
-    p.nt = nt;
-    p.n = static_cast<int>(min(static_cast<long long>(nt - p.j0), g1 - g));
-    g += p.n;
+  __device__ __forceinline__ bool next(Piece& pc) {
+    if (left <= 0) return false;
+    settle();
+    pc.b = p.b;
+    pc.unit = p.unit;
+    pc.len = p.len;
+    pc.nt = p.nt;
+    pc.j0 = p.j;
+    pc.n = min(p.nt - p.j, left);
+    p.j += pc.n;
+    left -= pc.n;
     return true;
   }
 };
 
-// Page ids of a CTA's tiles, 32 at a time: lane (u, i) has page i of tile
-// t0 + u, with ids of the next batch fetched while this one is used.
+// Page ids of a CTA's tiles, 32 at a time: lane (u, i) has page i of tile u of
+// the batch.  The next batch's ids are fetched while this one's are used.
 template <int TILE>
 struct PageBatch {
-  const PagedArgs& a;
   Walk<TILE> w;
-  long long g0;
-  int n, per_tile, tiles, u, i;
-  __device__ __forceinline__ PageBatch(const PagedArgs& a_, long long g0_, int n_, int b0, long long base0, int lane)
-      : a(a_), w(a_, g0_, g0_ + n_, b0, base0), g0(g0_), n(n_) {
-    per_tile = TILE / a.page;
-    tiles = 32 / per_tile;
-    u = lane / per_tile;
-    i = lane - u * per_tile;
+  int per_tile, tiles, u, i;
+  __device__ __forceinline__ PageBatch(const PagedArgs& a, const Place& start, int n, int lane) : w(a, start, n) {
+    const int shift = 31 - __clz(TILE / a.page);
+    per_tile = 1 << shift;
+    tiles = 32 >> shift;
+    u = lane >> shift;
+    i = lane & (per_tile - 1);
+    w.p.j += u;
+    w.left -= u;
   }
-  // (page, KV head) row of this lane's page in the batch that starts at tile
-  // t0: -1 where the tile has no such page, -2 where the table names none.
-  __device__ __forceinline__ long long fetch(int t0) {
-    const int t = t0 + u;
-    if (t >= n) return -1;
-    int unit, j;
-    w.seek(g0 + t, unit, j);
-    const int lp = j * per_tile + i;
-    if (lp * a.page >= w.len) return -1;
-    const int id = a.block_table[static_cast<size_t>(w.b) * a.max_pages + lp];
-    if (id < 0 || id >= a.num_pages) return -2;
-    return static_cast<long long>(id) * a.Hkv + unit / a.row_tiles;
+  // (page, KV head) row of this lane's page in the next batch: -1 where the
+  // tile has no such page, -2 where the table names none of the cache's.
+  __device__ __forceinline__ int fetch() {
+    const PagedArgs& a = w.a;
+    if (w.left <= 0) return -1;
+    w.settle();
+    const int lp = w.p.j * per_tile + i;
+    int row = -1;
+    if (lp * a.page < w.p.len) {
+      const int id = a.block_table[static_cast<size_t>(w.p.b) * a.max_pages + lp];
+      row = id >= 0 && id < a.num_pages ? id * a.Hkv + kv_head(a, w.p.unit) : -2;
+    }
+    w.p.j += tiles;
+    w.left -= tiles;
+    return row;
   }
 };
 
@@ -290,77 +344,82 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&b->kv_full[s], 2);
-      mbar_init(&b->kv_empty[s], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&b->q_full[i], 1);
-      mbar_init(&b->q_empty[i], 9);
-      mbar_init(&b->s_full[i], 1);
-      mbar_init(&b->s_free[i], 8);
-      mbar_init(&b->p_full[i], 8);
-      mbar_init(&b->pv_done[i], 1);
-      mbar_init(&b->o_full[i], 1);
-      mbar_init(&b->o_free[i], 4);
-      mbar_init(&b->stats_full[i], 8);
-    }
-    b->abort = 0u;
-    fence_mbar_init();
-  }
   if (warp == 1) {
     tmem_alloc(&b->tmem_base, S::kTmemCols);
     tmem_relinquish();
+  } else if (warp == 2) {
+    if (lane < NS) {
+      mbar_init(&b->kv_full[lane], 2);
+      mbar_init(&b->kv_empty[lane], 1);
+    }
+    fence_mbar_init();
+  } else if (warp == 3) {
+    if (lane < 2) {
+      mbar_init(&b->q_full[lane], 1);
+      mbar_init(&b->q_empty[lane], 9);
+      mbar_init(&b->s_full[lane], 1);
+      mbar_init(&b->s_free[lane], 8);
+      mbar_init(&b->p_full[lane], 8);
+      mbar_init(&b->pv_done[lane], 1);
+      mbar_init(&b->o_full[lane], 1);
+      mbar_init(&b->o_free[lane], 4);
+      mbar_init(&b->stats_full[lane], 8);
+    }
+    if (lane == 0) b->abort = 0u;
+    fence_mbar_init();
+  } else if (warp >= 12) {
+    for (int i = threadIdx.x - 384; i < 256; i += 128) b->nan_keys[i >> 7][i & 127] = 0u;
   }
-  if (R == 8) {                                      // the zero rows of P^T
-    for (int i = threadIdx.x; i < 2 * U * 64; i += kPgThreads)
+  if (R == 8 && warp >= 4 && warp < 8) {             // the zero rows of P^T
+    for (int i = threadIdx.x - 128; i < 2 * U * 64; i += 128)
       *reinterpret_cast<uint4*>(sP + (i >> 6) * S::kPSub + 24 * 128 + (i & 63) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
-  // This CTA's share of all tiles, and the request that it begins in.
+  // What came before in the stream may have written any of the inputs; the
+  // merge may be set up while this kernel runs.
+  grid_dependency_wait();
+  grid_dependency_launch();
+  // This CTA's share of all tiles, and the place where it begins.  Tiles of one
+  // KV head are summed in 32 bits (there are fewer than table entries).
   const int chunk = (a.B + kPgThreads - 1) / kPgThreads;
   const int c0 = min(a.B, static_cast<int>(threadIdx.x) * chunk), c1 = min(a.B, c0 + chunk);
-  long long mine = 0;
+  unsigned mine = 0;
   for (int i = c0; i < c1; ++i) mine += (pg_len(a, i) + TILE - 1) / TILE;
-  long long upto = mine;
+  unsigned upto = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, m);
+    const unsigned y = __shfl_up_sync(0xffffffffu, upto, m);
     if (lane >= m) upto += y;
   }
   if (lane == 31) b->scan[warp] = upto;
   __syncthreads();
-  long long before = 0, total = 0;
+  unsigned before = 0, sum = 0;
 #pragma unroll
   for (int w = 0; w < kPgThreads / 32; ++w) {
-    if (w < warp) before += b->scan[w];
-    total += b->scan[w];
+    const unsigned x = b->scan[w];
+    if (w < warp) before += x;
+    sum += x;
   }
-  total *= a.units;
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long g0 = min(total, static_cast<long long>(blockIdx.x) * per), g1 = min(total, g0 + per);
-  {
-    long long first = (before + upto - mine) * a.units;
-    const long long last = (before + upto) * a.units;
-    if (g0 < g1 && first <= g0 && g0 < last) {
-      int i = c0;
-      for (;; ++i) {
-        const long long t = static_cast<long long>((pg_len(a, i) + TILE - 1) / TILE) * a.units;
-        if (g0 < first + t) break;
-        first += t;
-      }
-      b->start_b = i;
-      b->start_base = first;
+  const long long total = static_cast<long long>(sum) * a.units;
+  const int per = static_cast<int>((static_cast<unsigned long long>(total) + kPagedCtas - 1) / kPagedCtas);
+  const long long g0 = min(total, static_cast<long long>(blockIdx.x) * per);
+  const int n_tiles = static_cast<int>(min(total - g0, static_cast<long long>(per)));
+  long long first = static_cast<long long>(before + upto - mine) * a.units;
+  if (n_tiles > 0 && first <= g0 && g0 < first + static_cast<long long>(mine) * a.units) {
+    int i = c0, len = pg_len(a, c0), nt = (len + TILE - 1) / TILE;
+    while (g0 >= first + static_cast<long long>(nt) * a.units) {
+      first += static_cast<long long>(nt) * a.units;
+      len = pg_len(a, ++i);
+      nt = (len + TILE - 1) / TILE;
     }
+    const unsigned pos = static_cast<unsigned>(g0 - first), unit = pos / static_cast<unsigned>(nt);
+    b->start = Place{i, static_cast<int>(unit), static_cast<int>(pos - unit * nt), len, nt};
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = b->tmem_base;
-  const int n_tiles = static_cast<int>(g1 - g0);
-  const int b0 = b->start_b;
-  const long long base0 = b->start_base;
+  const Place start = b->start;
 
   if (n_tiles == 0) {
     // nothing but the empty requests below
@@ -370,17 +429,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     tma_prefetch_desc(&tmV);
     // the cache is streamed once, unless several row tiles read it
     const uint64_t pol = a.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
-    PageBatch<TILE> pb(a, g0, n_tiles, b0, base0, lane);
-    long long row = pb.fetch(0);
+    PageBatch<TILE> pb(a, start, n_tiles, lane);
+    int row = pb.fetch();
     bool ok = true;
     for (int t0 = 0; t0 < n_tiles && ok; t0 += pb.tiles) {
-      const long long next = pb.fetch(t0 + pb.tiles);
+      const int next = pb.fetch();
       const int m = min(pb.tiles, n_tiles - t0);
       if (row == -2) report_status(a.status, DEVSTATUS_BAD_PAGE, WAIT_PAGED_TABLE);
       const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
       for (int u = 0; u < m; ++u) {
         const int t = t0 + u, s = t % NS;
-        if (t >= NS && !mbar_wait_warp(&b->kv_empty[s], ((t / NS) + 1) & 1, wc, WAIT_PAGED_KV_EMPTY)) {
+        if (t >= NS && !pg_wait(&b->kv_empty[s], ((t / NS) + 1) & 1, wc, WAIT_PAGED_KV_EMPTY)) {
           ok = false;
           break;
         }
@@ -389,8 +448,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         __syncwarp();
         if (pb.u == u && row >= 0) {
           uint8_t* st = sKV + s * S::kStageBytes + pb.i * a.page * D;
-          tma_load_3d_hint(st, &tmK, &b->kv_full[s], 0, 0, static_cast<int>(row), pol);
-          tma_load_3d_hint(st + S::kTileBytes, &tmV, &b->kv_full[s], 0, 0, static_cast<int>(row), pol);
+          tma_load_3d_hint(st, &tmK, &b->kv_full[s], 0, 0, row, pol);
+          tma_load_3d_hint(st + S::kTileBytes, &tmV, &b->kv_full[s], 0, 0, row, pol);
         }
         __syncwarp();
       }
@@ -402,37 +461,26 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const uint64_t dV = pg_desc<D>(smem_u32(sKV + S::kTileBytes));              // V tiles, MN-major (A of O^T)
     const uint64_t dQ = pg_desc<D>(smem_u32(sQ));                               // queries, K-major (B)
     const uint64_t dP = sdesc_sw128(smem_u32(sP), 16, 1024);                    // P^T, K-major (B)
-    Walk<TILE> walk(a, g0, g1, b0, base0);
+    Walk<TILE> walk(a, start, n_tiles);
     Piece pc;
-    bool ok = true;
-    int g = 0, it = 0;
-    // O^T(ob) (+)= V^T P^T for the tile with ring index gg.
-    auto issue_pv = [&](int gg, int ob, bool first) -> bool {
-      const int pb = gg & 1;
-      if (first && it >= 2 && !mbar_wait_warp(&b->o_free[ob], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE)) return false;
-      if (!mbar_wait_warp(&b->p_full[pb], (gg >> 1) & 1, wc, WAIT_PAGED_P)) return false;
-      tc_fence_after();
-      const int s = gg % NS;
-#pragma unroll
-      for (int kt = 0; kt < S::kPvSteps; ++kt) {
-        const uint64_t va = uint64_t((s * S::kStageBytes + kt * 32 * D) >> 4);
-        const uint64_t po = uint64_t((pb * S::kPBytes + (kt >> 2) * S::kPSub + (kt & 3) * 32) >> 4);
-        mma_f8_ss_e(tmem + S::kColO + S::kPRows * ob, dV + va, dP + po, S::kIdO, (!first || kt > 0) ? 1u : 0u);
-      }
-      tc_commit_e(&b->pv_done[pb]);
-      tc_commit_e(&b->kv_empty[s]);
-      return true;
-    };
-    for (; ok && walk.next(pc); ++it) {
-      const int qb = it & 1, ob = it & 1;
-      if (!mbar_wait_warp(&b->q_full[qb], (it >> 1) & 1, wc, WAIT_PAGED_Q)) break;
-      for (int j = 0; j < pc.n; ++j, ++g) {
-        const int s = g % NS, sb = g & 1;
-        if (!mbar_wait_warp(&b->kv_full[s], (g / NS) & 1, wc, WAIT_PAGED_KV) ||
-            (g >= 2 && !mbar_wait_warp(&b->s_free[sb], ((g >> 1) + 1) & 1, wc, WAIT_PAGED_S_FREE))) {
-          ok = false;
-          break;
+    // Turn g issues S of tile g and PV of tile g - 1, which may belong to the
+    // piece before.
+    int it = -1, j = 0, n = 0;                       // tile g: piece, tile of the piece, its tiles
+    for (int g = 0; g <= n_tiles; ++g) {
+      const int prev_it = it;
+      const bool prev_first = j == 1, prev_last = j == n;      // of tile g - 1
+      if (g < n_tiles) {
+        if (j == n) {
+          walk.next(pc);
+          n = pc.n;
+          j = 0;
+          ++it;
         }
+        const int s = g % NS, sb = g & 1, qb = it & 1;
+        if ((j == 0 && !pg_wait(&b->q_full[qb], (it >> 1) & 1, wc, WAIT_PAGED_Q)) ||
+            !pg_wait(&b->kv_full[s], (g / NS) & 1, wc, WAIT_PAGED_KV) ||
+            (g >= 2 && !pg_wait(&b->s_free[sb], ((g >> 1) + 1) & 1, wc, WAIT_PAGED_S_FREE)))
+          break;
         tc_fence_after();
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -443,31 +491,42 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             mma_f8_ss_e(tmem + S::kColS + S::kQRows * (sb * U + u), dK + ka, dQ + qo, S::kIdS, ks > 0 ? 1u : 0u);
           }
         tc_commit_e(&b->s_full[sb]);
-        if (j == pc.n - 1) tc_commit_e(&b->q_empty[qb]);
-        if (j > 0 && !issue_pv(g - 1, ob, j == 1)) {
-          ok = false;
-          break;
-        }
+        if (++j == n) tc_commit_e(&b->q_empty[qb]);
       }
-      if (!ok || !issue_pv(g - 1, ob, pc.n == 1)) break;
-      tc_commit_e(&b->o_full[ob]);
+      if (g > 0) {
+        const int s = (g - 1) % NS, pb = (g - 1) & 1, ob = prev_it & 1;
+        if ((prev_first && prev_it >= 2 && !pg_wait(&b->o_free[ob], ((prev_it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE)) ||
+            !pg_wait(&b->p_full[pb], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_P))
+          break;
+        tc_fence_after();
+#pragma unroll
+        for (int kt = 0; kt < S::kPvSteps; ++kt) {
+          const uint64_t va = uint64_t((s * S::kStageBytes + kt * 32 * D) >> 4);
+          const uint64_t po = uint64_t((pb * S::kPBytes + (kt >> 2) * S::kPSub + (kt & 3) * 32) >> 4);
+          mma_f8_ss_e(tmem + S::kColO + S::kPRows * ob, dV + va, dP + po, S::kIdO, (!prev_first || kt > 0) ? 1u : 0u);
+        }
+        tc_commit_e(&b->pv_done[pb]);
+        tc_commit_e(&b->kv_empty[s]);
+        if (prev_last) tc_commit_e(&b->o_full[ob]);
+      }
     }
   } else if (warp == 2) {
     // --------------------------------------------------------- page scales
-    PageBatch<TILE> pb(a, g0, n_tiles, b0, base0, lane);
-    long long row = pb.fetch(0);
+    PageBatch<TILE> pb(a, start, n_tiles, lane);
+    int row = pb.fetch();
     float ks = row >= 0 ? a.k_scale[row] : 0.0f, vs = row >= 0 ? a.v_scale[row] : 0.0f;
     bool ok = true;
     for (int t0 = 0; t0 < n_tiles && ok; t0 += pb.tiles) {
-      const long long next = pb.fetch(t0 + pb.tiles);
+      const int next = pb.fetch();
       const int m = min(pb.tiles, n_tiles - t0);
-      // vs = 0 or tiny: the exponent takes 2^-60 and P the share vs / 2^-60
-      const float v = fmaxf(vs, 8.673617379884035e-19f);
-      const float4 f = row >= 0 ? make_float4(ks * a.c_log2, log2f(v), 1.0f / v, vs / v * kBase)
+      // the exponent takes vs's power of two (2^-60 for 0 and what is smaller), P the rest
+      const int e = min(max(static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 127, -60), 100);
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const float4 f = row >= 0 ? make_float4(ks * a.c_log2, static_cast<float>(e), inv, vs * inv * kBase)
                                 : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
       for (int u = 0; u < m; ++u) {
         const int t = t0 + u, s = t % NS;
-        if (t >= NS && !mbar_wait_warp(&b->kv_empty[s], ((t / NS) + 1) & 1, wc, WAIT_PAGED_SC_EMPTY)) {
+        if (t >= NS && !pg_wait(&b->kv_empty[s], ((t / NS) + 1) & 1, wc, WAIT_PAGED_SC_EMPTY)) {
           ok = false;
           break;
         }
@@ -481,60 +540,51 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------- queries
-    constexpr int kWords = D / 64;                   // 32-bit words (two elements) of a row per lane
-    Walk<TILE> walk(a, g0, g1, b0, base0);
+    // Eight rows at a time, four lanes to a row; the code of all roles together
+    // should stay in the instruction cache, so its loops are not unrolled.
+    constexpr int kChunks = D / 32;                  // 16-byte groups of eight elements per lane
+    Walk<TILE> walk(a, start, n_tiles);
     Piece pc;
     for (int it = 0; walk.next(pc); ++it) {
       const int qb = it & 1;
-      if (it >= 2 && !mbar_wait_warp(&b->q_empty[qb], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_Q_EMPTY)) break;
-      const int hk = pc.unit / a.row_tiles;
+      if (it >= 2 && !pg_wait(&b->q_empty[qb], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_Q_EMPTY)) break;
+      const int hk = kv_head(a, pc.unit);
       const int r0 = (pc.unit - hk * a.row_tiles) * R;
-      const uint32_t* q = static_cast<const uint32_t*>(a.q) +
-                          (static_cast<size_t>(pc.b) * a.Hkv + hk) * a.rows * (D / 2) + static_cast<size_t>(r0) * (D / 2);
+      const uint4* q = static_cast<const uint4*>(a.q) +
+                       ((static_cast<size_t>(pc.b) * a.Hkv + hk) * a.rows + r0) * (D / 8) + (lane & 3) * kChunks;
       uint8_t* dst = sQ + qb * S::kQBytes;
+#pragma unroll 1
+      for (int r = lane >> 2; r < R; r += 8) {
+        uint4 w[kChunks];
+        uint32_t top = 0;
 #pragma unroll
-      for (int rg = 0; rg < R; rg += 8) {
-        uint32_t w[8][kWords];
+        for (int c = 0; c < kChunks; ++c) w[c] = r0 + r < a.rows ? q[static_cast<size_t>(r) * (D / 8) + c] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-          for (int c = 0; c < kWords; ++c)
-            w[r][c] = r0 + rg + r < a.rows ? q[static_cast<size_t>(rg + r) * (D / 2) + lane * kWords + c] : 0u;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int c = 0; c < kWords; ++c) top = max(top, max(w[r][c] & 0x7fffu, (w[r][c] >> 16) & 0x7fffu));
-          top = __reduce_max_sync(0xffffffffu, top);
-          // the row times 2^-e has its largest element in [128, 256)
-          const int e = min(max(static_cast<int>(top >> 7) - 134, -110), 121);
-          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          uint32_t hi = 0, lo = 0;
-#pragma unroll
-          for (int c = 0; c < kWords; ++c) {
-            const float x = __uint_as_float(w[r][c] << 16) * inv, y = __uint_as_float(w[r][c] & 0xffff0000u) * inv;
-            const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-            const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2((x - hf.x) * 16.0f, (y - hf.y) * 16.0f),
-                                                        __NV_SATFINITE, __NV_E4M3);
-            hi |= h << (16 * c);
-            lo |= l << (16 * c);
-          }
-          const int byte = lane * kWords * 2;
-          const int hr_off = pg_unit<D>(rg + r, byte >> 4) + (byte & 15);
-          const int lr_off = pg_unit<D>(R + rg + r, byte >> 4) + (byte & 15);
-          if (kWords == 2) {
-            *reinterpret_cast<uint32_t*>(dst + hr_off) = hi;
-            *reinterpret_cast<uint32_t*>(dst + lr_off) = lo;
-          } else {
-            *reinterpret_cast<uint16_t*>(dst + hr_off) = static_cast<uint16_t>(hi);
-            *reinterpret_cast<uint16_t*>(dst + lr_off) = static_cast<uint16_t>(lo);
-          }
-          // a row that holds something not finite has no scores
-          if (lane == 0)
-            b->q_factor[qb][rg + r] = top >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        for (int c = 0; c < kChunks; ++c) {
+          const uint32_t x = __vmaxu2(__vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu),
+                                      __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu));
+          top = max(top, max(x & 0xffffu, x >> 16));
         }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the row times 2^-e has its largest element in [128, 256)
+        const int e = min(max(static_cast<int>(top >> 7) - 134, -110), 121);
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) split_pair(x[k], inv, hi[k], lo[k]);
+          const int unit = (lane & 3) * (D / 64) + (c >> 1);
+          *reinterpret_cast<uint2*>(dst + pg_unit<D>(r, unit) + (c & 1) * 8) =
+              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(dst + pg_unit<D>(R + r, unit) + (c & 1) * 8) =
+              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        }
+        // a row that holds something not finite has no scores
+        if ((lane & 3) == 0)
+          b->q_factor[qb][r] = top >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -549,7 +599,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const int hr = half * H;                         // this group's first row
     const uint32_t lane_base = tmem + (uint32_t(wq * 32) << 16);
     const int page_shift = 31 - __clz(a.page);
-    Walk<TILE> walk(a, g0, g1, b0, base0);
+    Walk<TILE> walk(a, start, n_tiles);
     Piece pc;
     // A warp whose wait ran out goes on without waiting or arriving, so that
     // the group's hardware barriers are still met by all four warps.
@@ -557,18 +607,18 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     int g = 0, it = 0;
     for (; walk.next(pc); ++it) {
       const int ob = it & 1, qb = it & 1;
-      const int row0 = (pc.unit % a.row_tiles) * R + hr;
+      const int row0 = (a.row_tiles == 1 ? 0 : pc.unit % a.row_tiles) * R + hr;
       float m_used[H], l_t[H];
 #pragma unroll
       for (int r = 0; r < H; ++r) {
         m_used[r] = -INFINITY;
         l_t[r] = 0.0f;
       }
-      // the queries' factors are this warp's to read from here on
-      ok = ok && mbar_wait_warp(&b->q_full[qb], (it >> 1) & 1, wc, WAIT_PAGED_Q);
       for (int j = 0; j < pc.n; ++j, ++g) {
         const int sb = g & 1, st = g % NS;
-        ok = ok && mbar_wait2_warp(&b->kv_full[st], (g / NS) & 1, &b->s_full[sb], (g >> 1) & 1, wc, WAIT_PAGED_S);
+        // with S come the page factors (kv_full) and the queries' factors (q_full)
+        ok = ok && pg_wait3(&b->kv_full[st], (g / NS) & 1, &b->q_full[qb], (it >> 1) & 1, &b->s_full[sb],
+                                   (g >> 1) & 1, wc, WAIT_PAGED_S);
         tc_fence_after();
         const int tile0 = (pc.j0 + j) * TILE;
         float s[U][H];
@@ -607,6 +657,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
         }
         if (a.causal && tile0 + TILE > pc.len - a.Nq + 1) {
+          // V codes that are NaN must not meet p = 0 either: of a key that not
+          // every query sees they are cleared here, and noted for the epilogue
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int kt = 128 * u + wq * 32 + lane;
+            const int edge = tile0 + kt - (pc.len - a.Nq + 1);
+            if (edge >= 0 && tile0 + kt < pc.len)
+              ok = clear_nan_codes<D>(sKV + st * S::kStageBytes + S::kTileBytes, kt, half, edge, b->nan_keys[ob],
+                                      &b->o_free[ob], it, ok, wc);
+          }
+          ok = __all_sync(0xffffffffu, ok);
           int i = row0 % a.Nq;                       // query of row r
 #pragma unroll
           for (int r = 0; r < H; ++r) {
@@ -644,7 +705,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             l_t[r] *= alpha[r];
           }
           if (j > 0) {   // O^T holds earlier tiles of this piece: rescale it once PV(g-1) is done
-            ok = ok && mbar_wait_warp(&b->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_PV);
+            ok = ok && pg_wait(&b->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_PV);
             tc_fence_after();
             if (ok) {
 #pragma unroll
@@ -701,10 +762,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         if (ok && lane == 0) mbar_arrive(&b->p_full[pb]);
       }
       if (ok && lane == 0) mbar_arrive(&b->q_empty[qb]);
-      // Piece done: once its last PV has completed (which also orders these
-      // writes after the epilogue's read of this stats buffer two pieces ago),
-      // publish the running max and the per-warp sums.
-      ok = ok && mbar_wait_warp(&b->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_PV);
+      // Piece done: publish the running max and the per-warp sums, once the
+      // epilogue has let go of this buffer two pieces ago.
+      if (it >= 2) ok = ok && pg_wait(&b->o_free[ob], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE);
 #pragma unroll
       for (int r = 0; r < H; ++r) {
         const float l = warp_sum(l_t[r]);
@@ -724,24 +784,39 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // lane; M = 64 puts rows 16w..16w+15 in lanes 0-15 of quarter w.
     const int drow = (D == 128) ? wq * 32 + lane : (lane < 16 ? wq * 16 + lane : -1);
     PagedNote note{-1, 0, 0, 0};
-    Walk<TILE> walk(a, g0, g1, b0, base0);
+    Walk<TILE> walk(a, start, n_tiles);
     Piece pc;
-    for (int it = 0;; ++it) {
-      const long long at = walk.g;
-      if (!walk.next(pc)) break;
+    for (int it = 0; walk.next(pc); ++it) {
       const int ob = it & 1;
-      if (!mbar_wait_warp(&b->o_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_O) ||
-          !mbar_wait_warp(&b->stats_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_STATS))
-        break;
-      tc_fence_after();
+      if (!pg_wait(&b->stats_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_STATS)) break;
       const bool whole = pc.n == pc.nt;
       const int slot = 2 * blockIdx.x + (pc.j0 > 0 ? 0 : 1);
-      if (pc.j0 > 0 && pc.j0 + pc.n == pc.nt) note = PagedNote{pc.b, pc.unit, static_cast<int>((at - pc.j0) / per), 0};
-      const int hk = pc.unit / a.row_tiles;
+      // a unit that an earlier CTA began is this CTA's first piece: it began
+      // ceil(j0 / per) shares before
+      if (pc.j0 > 0 && pc.j0 + pc.n == pc.nt)
+        note = PagedNote{pc.b, pc.unit, static_cast<int>(blockIdx.x) - (pc.j0 + per - 1) / per, 0};
+      const int hk = kv_head(a, pc.unit);
       const int row0 = (pc.unit - hk * a.row_tiles) * R;
+      const int rows = min(R, a.rows - row0);
       const size_t out = (static_cast<size_t>(pc.b) * a.Hkv + hk) * a.rows + row0;
+      // lane r has row r's sum
+      float inv = 0.0f;
+      if (lane < rows) {
+        const float L = b->stat_l[ob][0][lane] + b->stat_l[ob][1][lane] + b->stat_l[ob][2][lane] + b->stat_l[ob][3][lane];
+        inv = L == 0.0f ? 0.0f : (1.0f / kBase) / L;
+        if (wq == 0) {
+          const float lse = L == 0.0f ? -INFINITY : (b->stat_m[ob][lane] + log2f(L)) * kLn2;
+          if (whole)
+            a.lse[out + lane] = lse;
+          else
+            a.part_lse[slot * R + lane] = lse;
+        }
+      }
+      if (!pg_wait(&b->o_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_O)) break;
+      tc_fence_after();
+      const uint32_t bad = drow >= 0 ? b->nan_keys[ob][drow] : 0u;
       constexpr int kStep = R == 8 ? 8 : 16;
-#pragma unroll
+#pragma unroll 1
       for (int rg = 0; rg < R; rg += kStep) {
         float o[kStep];
         if constexpr (R == 8) {
@@ -764,25 +839,34 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[r] += __uint_as_float(x[r]);
         }
-        if (drow >= 0) {
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          const float f = __shfl_sync(0xffffffffu, inv, rg + k);
+          o[k] = f == 0.0f ? 0.0f : o[k] * f;
+        }
+        if (bad != 0u) {     // query i sees the boundary keys 0..i-1
+          int i = (row0 + rg) % a.Nq;
 #pragma unroll
           for (int k = 0; k < kStep; ++k) {
-            const int r = rg + k;
-            if (row0 + r < a.rows) {
-              const float L = b->stat_l[ob][0][r] + b->stat_l[ob][1][r] + b->stat_l[ob][2][r] + b->stat_l[ob][3][r];
-              const float val = L == 0.0f ? 0.0f : o[k] * (1.0f / kBase) / L;
-              const float lse = L == 0.0f ? -INFINITY : (b->stat_m[ob][r] + log2f(L)) * kLn2;
-              if (whole) {
-                static_cast<__nv_bfloat16*>(a.o)[(out + r) * D + drow] = __float2bfloat16_rn(val);
-                if (drow == 0) a.lse[out + r] = lse;
-              } else {
-                a.part_o[(static_cast<size_t>(slot) * R + r) * D + drow] = val;
-                if (drow == 0) a.part_lse[slot * R + r] = lse;
-              }
-            }
+            if (bad & ((1u << i) - 1u)) o[k] = NAN;
+            i = i + 1 == a.Nq ? 0 : i + 1;
+          }
+        }
+        if (drow >= 0) {
+          if (whole) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (out + rg) * D + drow;
+#pragma unroll
+            for (int k = 0; k < kStep; ++k)
+              if (rg + k < rows) dst[k * D] = __float2bfloat16_rn(o[k]);
+          } else {
+            float* dst = a.part_o + (static_cast<size_t>(slot) * R + rg) * D + drow;
+#pragma unroll
+            for (int k = 0; k < kStep; ++k)
+              if (rg + k < rows) dst[k * D] = o[k];
           }
         }
       }
+      if (bad != 0u) b->nan_keys[ob][drow] = 0u;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->o_free[ob]);
@@ -793,7 +877,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   // requests without a token
   if (warp >= 12) {
     const int t = threadIdx.x - 384;
-    for (int i = blockIdx.x; i < a.B; i += gridDim.x) {
+    for (int i = blockIdx.x; i < a.B; i += kPagedCtas) {
       if (pg_len(a, i) > 0) continue;
       const size_t rows = static_cast<size_t>(a.Hkv) * a.rows;
       for (size_t c = t; c < rows * (D / 8); c += 128)
@@ -811,89 +895,98 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 }
 
 // O = sum_s exp(LSE_s - LSE) O_s with LSE = log sum_s exp(LSE_s) over the
-// pieces of a unit that CTA `x` ended: its own and those of the CTAs before it
-// down to the one that began it.  One block per (CTA, row of the unit);
-// thread = (output column, one of kParts interleaved subsets of the pieces).
+// pieces of a unit that CTA blockIdx.x ended: its own and those of the CTAs
+// before it down to the one that began it.  A warp per row; the pieces are
+// added in order.
 constexpr int kMergeThreads = 256;
 
 template <int D, int R>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a) {
-  constexpr int kParts = kMergeThreads / D;
-  __shared__ float red[kMergeThreads / 32];
-  __shared__ float acc_s[kParts][D];
-  __shared__ float l_s[kParts];
-  const int cta = blockIdx.x, r = blockIdx.y;
-  const PagedNote note = a.notes[cta];
+  constexpr int kVec = D / 32;                       // columns per lane
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);   // row of the unit
+  grid_dependency_wait();
+  const PagedNote note = a.notes[blockIdx.x];
   if (note.b < 0) return;
-  const int hk = note.unit / a.row_tiles;
+  const int hk = kv_head(a, note.unit);
   const int row = (note.unit - hk * a.row_tiles) * R + r;
   if (row >= a.rows) return;
-  const int ns = cta - note.first + 1;
-  const int c = threadIdx.x % D, part = threadIdx.x / D;
+  const int ns = blockIdx.x - note.first + 1;
   // the first piece is in its CTA's second slot, the others in the first
   auto slot = [&](int s) { return static_cast<size_t>(2 * (note.first + s) + (s == 0 ? 1 : 0)) * R + r; };
-  float m = -INFINITY;
-  bool bad = false;                                   // NaN must not hide from the maximum
-  for (int s = threadIdx.x; s < ns; s += kMergeThreads) {
+  float m = -INFINITY, L = 0.0f;
+  bool bad = false;                                  // NaN must not hide from the maximum
+  for (int s = lane; s < ns; s += 32) {
     const float x = a.part_lse[slot(s)];
     bad |= x != x;
     m = fmaxf(m, x);
   }
   m = redux_max(m);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-  bad = __syncthreads_or(bad);
-#pragma unroll
-  for (int w = 0; w < kMergeThreads / 32; ++w) m = fmaxf(m, red[w]);
-  float L = 0.0f, acc = 0.0f;
+  bad = __any_sync(0xffffffffu, bad);
+  float acc[kVec] = {};
   if (m != -INFINITY) {
-#pragma unroll 4
-    for (int s = part; s < ns; s += kParts) {
-      const float wgt = ex2_approx((a.part_lse[slot(s)] - m) * 1.4426950408889634f);
-      L += wgt;
-      acc = fmaf(wgt, a.part_o[slot(s) * D + c], acc);
-    }
-  }
-  acc_s[part][c] = acc;
-  if (c == 0) l_s[part] = L;
-  __syncthreads();
-  if (part == 0) {
-    float at = 0.0f, lt = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < ns; ++s) {
+      const size_t at = slot(s);
+      const float w = ex2_approx((a.part_lse[at] - m) * kLog2e);
+      L += w;
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-      at += acc_s[p][c];
-      lt += l_s[p];
+      for (int c = 0; c < kVec; c += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * kVec + c);
+        acc[c] = fmaf(w, x.x, acc[c]);
+        acc[c + 1] = fmaf(w, x.y, acc[c + 1]);
+      }
     }
-    const size_t out = (static_cast<size_t>(note.b) * a.Hkv + hk) * a.rows + row;
-    static_cast<__nv_bfloat16*>(a.o)[out * D + c] = __float2bfloat16_rn(bad ? NAN : lt > 0.0f ? at / lt : 0.0f);
-    if (c == 0) a.lse[out] = bad ? NAN : lt > 0.0f ? m + log2f(lt) * kLn2 : -INFINITY;
   }
+  const float inv = bad ? NAN : L > 0.0f ? 1.0f / L : 0.0f;
+  const size_t out = (static_cast<size_t>(note.b) * a.Hkv + hk) * a.rows + row;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + out * D + lane * kVec);
+#pragma unroll
+  for (int c = 0; c < kVec; c += 2) dst[c / 2] = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+  if (lane == 0) a.lse[out] = bad ? NAN : L > 0.0f ? m + log2f(L) * kLn2 : -INFINITY;
 }
 
 template <int D, int R>
-cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t stream) {
   constexpr size_t smem = pg_smem_bytes<D, R>();
   static_assert(smem <= 227 * 1024, "shared memory budget");
   auto kern = decode_paged_kernel<D, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kPgThreads, smem, stream>>>(tk, tv, a);
-  e = cudaGetLastError();
+  e = cudaFuncSetAttribute(paged_merge_kernel<D, R>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<D, R><<<dim3(ctas, R < a.rows ? R : a.rows), kMergeThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  // Both kernels may be set up before the one ahead of them in the stream has
+  // ended; each waits for it before its first access to memory.
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kPagedCtas);
+  cfg.blockDim = dim3(kPgThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(kPagedCtas, ((a.rows < R ? a.rows : R) + 7) / 8);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, R>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int d, int row_tile,
-                                int ctas, cudaStream_t stream) {
+                                cudaStream_t stream) {
   if (d == 64)
-    return row_tile == 8    ? launch_paged_t<64, 8>(tk, tv, a, ctas, stream)
-           : row_tile == 16 ? launch_paged_t<64, 16>(tk, tv, a, ctas, stream)
-                            : launch_paged_t<64, 32>(tk, tv, a, ctas, stream);
-  return row_tile == 8    ? launch_paged_t<128, 8>(tk, tv, a, ctas, stream)
-         : row_tile == 16 ? launch_paged_t<128, 16>(tk, tv, a, ctas, stream)
-                          : launch_paged_t<128, 32>(tk, tv, a, ctas, stream);
+    return row_tile == 8    ? launch_paged_t<64, 8>(tk, tv, a, stream)
+           : row_tile == 16 ? launch_paged_t<64, 16>(tk, tv, a, stream)
+                            : launch_paged_t<64, 32>(tk, tv, a, stream);
+  return row_tile == 8    ? launch_paged_t<128, 8>(tk, tv, a, stream)
+         : row_tile == 16 ? launch_paged_t<128, 16>(tk, tv, a, stream)
+                          : launch_paged_t<128, 32>(tk, tv, a, stream);
 }
 
 }  // namespace fa

@@ -243,6 +243,7 @@ struct TableArgs {
 cudaError_t launch_page_tables(const TableArgs& a, cudaStream_t stream);
 
 // Attention over the 8-bit paged cache (fa_decode_paged.cu).
+constexpr int kPagedCtas = 148;   // one per SM of a B200; more or fewer SMs only change how they are shared out
 struct PagedNote {     // a CTA ended unit (b, unit), which CTA `first` began (b < 0: it ended none that it did not begin)
   int b, unit, first, pad;
 };
@@ -268,7 +269,7 @@ struct PagedArgs {
 };
 // tk, tv: maps over the codes as [num_pages * Hkv, page, d], box one page, swizzled over d bytes.
 cudaError_t launch_decode_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int d, int row_tile,
-                                int ctas, cudaStream_t stream);
+                                cudaStream_t stream);
 
 cudaError_t launch_watchdog_selftest(uint64_t limit_ns, cudaStream_t stream);
 

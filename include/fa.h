@@ -415,8 +415,8 @@ FA_API fa_status fa_cache_append_fp8(const void* k, const void* v, const int* sl
  * A row that sees no key (length 0, or causal with i < Nq - seq_lens[b]) gets
  * O = 0 and LSE = -inf.  Bytes of the cache at or behind a request's length
  * have no effect, whatever they are.  A key or query with a NaN makes the rows
- * that see it NaN.  The scales that count must be finite, 0 or within
- * 2^-60..2^60 in size.
+ * that see it NaN, a value's NaN those rows' outputs in its column.  The
+ * scales that count must be finite, 0 or within 2^-60..2^60.
  */
 FA_API fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache,
                                          const float* k_scale, const float* v_scale, const int* block_table,

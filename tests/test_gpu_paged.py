@@ -384,6 +384,35 @@ def nan_rows(ref, rows):
     return ref
 
 
+@pytest.mark.parametrize("lens", [[300, 3, 130], [128, 257, 5000]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_nan_value_of_a_newer_token(d, lens):
+    """NaN codes in the values of the newest tokens: only the queries that see those tokens become NaN, in
+    those columns alone, over many requests per CTA and over a tile's and a CTA's border."""
+    B, Nq = 3 * 60, 4
+    q, kc, vc, ks, vs, table, n = decode_case(B, 4, 2, Nq, d, 16, lens * 60, seed=86, stale=False)
+    rng = np.random.default_rng(87)
+    clean = vc[0].copy()
+    hits = []
+    for b in range(B):
+        for back in rng.choice(Nq, 2, replace=False) if b % 4 else []:
+            j = int(n[b]) - 1 - back
+            if j < 0:
+                continue
+            hk, col = int(rng.integers(2)), int(rng.integers(d))
+            vc[0][table[b, j // 16], hk, j % 16, col] = (0x7F, 0xFF)[b % 2]
+            clean[table[b, j // 16], hk, j % 16, col] = 0
+            hits.append((b, hk, j, col))
+    vc[1].copy_(torch.from_numpy(vc[0]))
+    ref = paged.decode_paged(q[0], kc[0], clean, ks[0], vs[0], table, n, d ** -0.5, True)
+    for b, hk, j, col in hits:
+        for i in range(Nq):
+            if j <= n[b] - Nq + i:
+                ref[0][b, 2 * hk:2 * hk + 2, i, col] = np.nan
+    assert np.isnan(ref[0]).any() and len(hits) > 100
+    check_decode(q, kc, vc, ks, vs, table, n, d ** -0.5, True, d, want=ref)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_skips_pages_outside_the_cache(d):
     case = list(decode_case(2, 4, 2, 1, d, 16, [900, 40], seed=82, stale=False))
