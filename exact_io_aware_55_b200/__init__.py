@@ -280,27 +280,41 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _on_device(fn, device, stream, *args):
-    """Calls fn(*args, stream) with `device` current, on `stream` or that device's current stream."""
-    if device.index != torch.cuda.current_device():
+def _launch(fn, device: int, stream, *args):
+    """Calls fn(*args, stream) with GPU `device` current, on `stream` or that GPU's current stream."""
+    if device == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
+    else:
         with torch.cuda.device(device):
-            return check(fn(*args, (stream or torch.cuda.current_stream()).cuda_stream))
-    return check(fn(*args, (stream or torch.cuda.current_stream()).cuda_stream))
+            st = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
+    if st != FA_OK:
+        check(st)
+
+
+# A decode step makes these calls once per layer and token, so the checks are written for few Python steps.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check_as(t, name, shape, dtypes, device):
-    if t.device != device or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {' or '.join(str(x) for x in dtypes)} {tuple(shape)} on {device}, "
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name}: expected contiguous {' or '.join(str(x) for x in dtypes)} {tuple(shape)} on cuda:{device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _cuda_device(t):
-    if t.device.type != "cuda":
+def _gpu_index(t):
+    if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
-    return t.device
+    return t.get_device()
 
 
-_I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+def _dims(t):
+    if t.dim() != 4:
+        raise ValueError("tensors must be [B, H, N, d]")
+    return t.shape
+
+
+_Strides = ctypes.c_longlong * 3
+_I32, _F32, _F64, _BF16 = (torch.int32,), (torch.float32,), (torch.float64,), (torch.bfloat16,)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -320,30 +334,33 @@ def fa_rope(x, y, positions, inv_freq, factor: float = 1.0, interleaved: bool = 
             stream=None) -> None:
     """y <- x [B,H,N,d] bf16 with rotary positions on its first 2 * len(inv_freq) elements.  x and y may have any
     batch, head and token strides (d contiguous); y may be x.  positions: int32 [B,N], or None for 0..N-1."""
-    B, H, N, d = _shape(x)
-    dev = _cuda_device(x)
-    for t in (x, y):
-        if t.dtype != torch.bfloat16 or t.shape != x.shape or t.device != dev or (t.stride(3) != 1 and d > 1):
-            raise ValueError(f"expected bf16 {tuple(x.shape)} on {dev} with d contiguous, got {t.dtype} {tuple(t.shape)}")
+    B, H, N, d = shape = _dims(x)
+    dev = _gpu_index(x)
+    xb, xh, xn, xd = x.stride()
+    yb, yh, yn, yd = y.stride() if y.dim() == 4 else (0, 0, 0, 0)
+    if x.dtype is not torch.bfloat16 or y.dtype is not torch.bfloat16 or y.shape != shape or y.get_device() != dev \
+            or xd != 1 or yd != 1:
+        raise ValueError(f"x and y must be bf16 of one shape on one GPU with d contiguous, got {x.dtype} {tuple(shape)} "
+                         f"on {x.device} and {y.dtype} {tuple(y.shape)} on {y.device}")
     if positions is not None:
         _check_as(positions, "positions", (B, N), _I32, dev)
-    _check_as(inv_freq, "inv_freq", (inv_freq.numel(),), (torch.float64,), dev)
-    xs = (ctypes.c_longlong * 3)(*x.stride()[:3])
-    ys = (ctypes.c_longlong * 3)(*y.stride()[:3])
-    _on_device(lib.fa_rope, dev, stream, x.data_ptr(), y.data_ptr(), _ptr(positions), inv_freq.data_ptr(), factor,
-               B, H, N, d, 2 * inv_freq.numel(), int(bool(interleaved)), int(bool(transpose)), xs, ys)
+    pairs = inv_freq.numel()
+    _check_as(inv_freq, "inv_freq", (pairs,), _F64, dev)
+    _launch(lib.fa_rope, dev, stream, x.data_ptr(), y.data_ptr(), 0 if positions is None else positions.data_ptr(),
+            inv_freq.data_ptr(), factor, B, H, N, d, 2 * pairs, 1 if interleaved else 0, 1 if transpose else 0,
+            _Strides(xb, xh, xn), _Strides(yb, yh, yn))
 
 
 def rope_forward(x, positions, inv_freq, interleaved: bool = False, factor: float = 1.0, stream=None):
     """Rotary positions on x, as a new contiguous tensor."""
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     fa_rope(x, y, positions, inv_freq, factor, interleaved, False, stream)
     return y
 
 
 def rope_backward(dy, positions, inv_freq, interleaved: bool = False, factor: float = 1.0, stream=None):
     """Gradient of rope_forward with respect to x, as a new contiguous tensor."""
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
     fa_rope(dy, dx, positions, inv_freq, factor, interleaved, True, stream)
     return dx
 
@@ -353,7 +370,7 @@ def fa_page_tables(ctx_lens, new_lens, free_pages, free_head, block_table, slots
     """Grows (new_lens >= 0) or finishes (new_lens < 0) the requests of a batch: takes pages from free_pages,
     writes block_table, slots, positions, seq_lens and free_head_out.  All int32; seq_lens may be ctx_lens and
     free_head_out may be free_head."""
-    dev = _cuda_device(ctx_lens)
+    dev = _gpu_index(ctx_lens)
     if slots.dim() != 2 or block_table.dim() != 2:
         raise ValueError("slots must be [B, N] and block_table [B, max_pages]")
     B, N = slots.shape
@@ -365,7 +382,7 @@ def fa_page_tables(ctx_lens, new_lens, free_pages, free_head, block_table, slots
                            (positions, "positions", (B, N)), (seq_lens, "seq_lens", (B,)),
                            (free_head_out, "free_head_out", (1,))):
         _check_as(t, name, shape, _I32, dev)
-    _on_device(lib.fa_page_tables, dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+    _launch(lib.fa_page_tables, dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
                free_head.data_ptr(), block_table.data_ptr(), slots.data_ptr(), positions.data_ptr(),
                seq_lens.data_ptr(), free_head_out.data_ptr(), B, N, n_free, max_pages, page_size)
 
@@ -373,9 +390,11 @@ def fa_page_tables(ctx_lens, new_lens, free_pages, free_head, block_table, slots
 def _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev):
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_pages, Hkv, page_size, d]")
-    pages, page = k_cache.shape[0], k_cache.shape[2]
-    _check_as(k_cache, "k_cache", (pages, Hkv, page, d), _E4M3, dev)
-    _check_as(v_cache, "v_cache", (pages, Hkv, page, d), _E4M3, dev)
+    pages, heads, page, depth = shape = k_cache.shape
+    if heads != Hkv or depth != d:
+        raise ValueError(f"k_cache: expected [num_pages, {Hkv}, page_size, {d}], got {tuple(shape)}")
+    _check_as(k_cache, "k_cache", shape, _E4M3, dev)
+    _check_as(v_cache, "v_cache", shape, _E4M3, dev)
     _check_as(k_scale, "k_scale", (pages, Hkv), _F32, dev)
     _check_as(v_scale, "v_scale", (pages, Hkv), _F32, dev)
     return pages, page
@@ -384,13 +403,13 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev):
 def fa_cache_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
     """Quantises k, v [B,Hkv,N,d] bf16 into the pages that slots [B,N] int32 names (negative: not written);
     k_cache, v_cache e4m3 [num_pages,Hkv,page_size,d], k_scale, v_scale fp32 [num_pages,Hkv]."""
-    B, Hkv, N, d = _shape(k)
-    dev = _cuda_device(k)
-    _check_as(k, "k", (B, Hkv, N, d), _BF16, dev)
-    _check_as(v, "v", (B, Hkv, N, d), _BF16, dev)
+    B, Hkv, N, d = shape = _dims(k)
+    dev = _gpu_index(k)
+    _check_as(k, "k", shape, _BF16, dev)
+    _check_as(v, "v", shape, _BF16, dev)
     _check_as(slots, "slots", (B, N), _I32, dev)
     pages, page = _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
-    _on_device(lib.fa_cache_append_fp8, dev, stream, k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
+    _launch(lib.fa_cache_append_fp8, dev, stream, k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
                v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, Hkv, N, d, pages, page)
 
 
@@ -405,11 +424,17 @@ def fa_fwd_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
                             causal: bool, workspace, stream=None) -> None:
     """O, LSE <- attention of q [B,H,Nq,d] (Nq <= 16) over the first seq_lens[b] tokens of each request's pages;
     block_table int32 [B,max_pages], seq_lens int32 [B], caches and scales as in fa_cache_append_fp8."""
-    B, H, Nq, d = _shape(q)
-    dev = _cuda_device(q)
-    _check_as(q, "q", (B, H, Nq, d), _BF16, dev)
-    _check_as(o, "o", (B, H, Nq, d), _BF16, dev)
-    _check_as(lse, "lse", (B, H, Nq), _F32, dev)
+    shape = _dims(q)
+    dev = _gpu_index(q)
+    _check_as(o, "o", shape, _BF16, dev)
+    _check_as(lse, "lse", shape[:3], _F32, dev)
+    _decode_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, scale, causal, workspace, stream, dev)
+
+
+def _decode_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, scale, causal, workspace, stream,
+                  dev):
+    B, H, Nq, d = shape = q.shape
+    _check_as(q, "q", shape, _BF16, dev)
     if k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_cache must be [num_pages, Hkv, page_size, d] and block_table [B, max_pages]")
     Hkv = k_cache.shape[1]
@@ -419,23 +444,24 @@ def fa_fwd_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     _check_as(seq_lens, "seq_lens", (B,), _I32, dev)
     wptr, wbytes = 0, 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
-        wptr, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _on_device(lib.fa_fwd_decode_paged_fp8, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-               k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-               lse.data_ptr(), B, H, Hkv, Nq, d, pages, page, max_pages, float(scale), int(bool(causal)), wptr, wbytes)
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+        wptr, wbytes = workspace.data_ptr(), workspace.nbytes
+    _launch(lib.fa_fwd_decode_paged_fp8, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), B, H, Hkv, Nq, d, pages, page, max_pages, scale, 1 if causal else 0, wptr, wbytes)
 
 
 def attention_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                                scale: float | None = None, causal: bool = False, workspace=None, stream=None):
     """Allocates O, LSE (and the workspace unless given) with torch and runs fa_fwd_decode_paged_fp8."""
-    B, H, Nq, d = _shape(q)
-    o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    B, H, Nq, d = _dims(q)
+    dev = _gpu_index(q)
+    o = torch.empty_like(q, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+    lse = torch.empty_strided((B, H, Nq), (H * Nq, Nq, 1), dtype=torch.float32, device=q.device)
     if workspace is None:
         n = fa_fwd_decode_paged_fp8_workspace_size(B, H, k_cache.shape[1], Nq, d)
         workspace = torch.empty(max(16, n), dtype=torch.uint8, device=q.device)
-    fa_fwd_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse,
-                            _default_scale(d) if scale is None else scale, causal, workspace, stream)
+    _decode_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse,
+                  _default_scale(d) if scale is None else scale, causal, workspace, stream, dev)
     return o, lse

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -600,10 +601,10 @@ bool cache_fits(int num_pages, int Hkv, int page_size) {
 
 // Paged decode: query rows that share a KV head go in tiles of 8, 16 or 32 (the
 // smallest that holds them; a row costs an exponential per key, used or not).
-// kPagedCtas CTAs with two slots for pieces and a note each.
+// kPagedCtas CTAs with two slots for pieces, and a mark for each slot.
 struct PagedPlan {
   int row_tile, row_tiles;
-  size_t lse_off, notes_off, total;
+  size_t lse_off, marks_off, total;
 };
 PagedPlan paged_plan(int H, int Hkv, int Nq, int d) {
   PagedPlan p{};
@@ -612,9 +613,24 @@ PagedPlan paged_plan(int H, int Hkv, int Nq, int d) {
   p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
   const size_t parts = size_t(2) * fa::kPagedCtas * p.row_tile;
   p.lse_off = parts * d * 4;
-  p.notes_off = p.lse_off + parts * 4;
-  p.total = p.notes_off + fa::kPagedCtas * sizeof(fa::PagedNote);
+  p.marks_off = p.lse_off + parts * 4;
+  p.total = p.marks_off + size_t(2) * fa::kPagedCtas * sizeof(unsigned long long);
   return p;
+}
+
+// A number that no other call of this process has, and that what a workspace
+// happens to hold is unlikely to be: a counter from a start taken from the
+// clock, through a bijection of 64 bits (odd multiplications and shifts).
+unsigned long long next_nonce() {
+  static std::atomic<unsigned long long> counter{static_cast<unsigned long long>(
+      std::chrono::steady_clock::now().time_since_epoch().count())};
+  unsigned long long x;
+  do {
+    x = counter.fetch_add(1, std::memory_order_relaxed) * 0x9e3779b97f4a7c15ull;
+    x = (x ^ (x >> 31)) * 0xbf58476d1ce4e5b9ull;
+    x ^= x >> 29;
+  } while (x == 0);
+  return x;
 }
 
 // 3-D tensor map over the codes of a paged cache [pages * heads, page, d], box
@@ -826,7 +842,8 @@ fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_lse = reinterpret_cast<float*>(ws + plan.lse_off);
-  a.notes = reinterpret_cast<fa::PagedNote*>(ws + plan.notes_off);
+  a.marks = reinterpret_cast<unsigned long long*>(ws + plan.marks_off);
+  a.nonce = next_nonce();
   a.B = B;
   a.Hkv = Hkv;
   a.Nq = Nq;

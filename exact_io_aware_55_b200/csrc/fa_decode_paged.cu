@@ -34,8 +34,8 @@
 // inside a unit.  A unit that lies within one CTA is written directly; of a
 // unit cut between CTAs each CTA leaves its normalised O and LSE in one of its
 // two slots of the workspace (one for a piece that does not begin its unit, one
-// for a piece that does), the CTA that ends the unit notes who took part, and
-// paged_merge_kernel combines them by their log-sum-exp.  No atomics: a call's
+// for a piece that does), and the CTA that is the last to finish a piece of the
+// unit combines them by their log-sum-exp, in the order of the pieces, so that
 // results do not depend on timing.
 //
 // Warps: 0 page ids and TMA, 1 MMA issuer and TMEM owner, 2 page scales,
@@ -46,6 +46,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -83,6 +85,10 @@ struct PgShape {
   static_assert(kCols <= 512, "TMEM columns");
 };
 
+// A unit to combine: row tile `unit` of request b, in pieces of CTAs first..last.
+struct Merge {
+  int b, unit, first, last;
+};
 // A place among the tiles: tile j of unit `unit` of request b, which has nt.
 struct Place {
   int b, unit, j, len, nt;
@@ -96,13 +102,16 @@ struct PgBarriers {
   uint64_t p_full[2], pv_done[2];
   uint64_t o_full[2], o_free[2];
   uint64_t stats_full[2];
+  uint64_t merged;
   alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, e, 2^-e, vs / 2^e
   alignas(16) float q_factor[2][R];        // power of two that a row of queries was divided by
   alignas(16) float red_max[4][R];         // per-warp tile maxima (log2 units)
   alignas(16) float stat_m[2][R];          // piece's running max
   alignas(16) float stat_l[2][4][R];       // piece's per-warp sums
   uint32_t nan_keys[2][128];               // per column of a piece: boundary keys whose V code is NaN
-  alignas(16) unsigned scan[kPgThreads / 32];
+  int per, n_tiles;
+  int n_merge;                             // units that this CTA is the last to have finished a piece of
+  Merge merge[2];
   Place start;
   uint32_t tmem_base;
   uint32_t abort;
@@ -148,6 +157,9 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
       : "memory");
   return y != 0;
 }
+// Other threads' global writes, seen by this one -> visible to its bulk copies.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 // Bounded waits.  The roles' code shares the SM's instruction cache, so only
 // the first look is inline.
 __device__ __noinline__ bool pg_wait_slow(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t where) {
@@ -164,10 +176,8 @@ __device__ __forceinline__ bool pg_wait3(uint64_t* x, uint32_t px, uint64_t* y, 
          (pg_wait_slow(x, px, w, where) && pg_wait_slow(y, py, w, where) && pg_wait_slow(z, pz, w, where));
 }
 
-// Programmatic dependent launch: wait for the grids before this one in the
-// stream, and let the one behind it be set up.
+// Programmatic dependent launch: wait for the grids before this one in the stream.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // N (4, 8, 16) consecutive TMEM columns of this thread's lane.
 template <int N>
@@ -327,6 +337,114 @@ struct PageBatch {
   }
 };
 
+// Marks this CTA's piece of a unit as done and looks whether all of them are,
+// by one warp, behind a barrier of the threads that wrote the piece.  A mark is
+// the call's nonce, so what the workspace held before is none.  Store, fence,
+// load: of the CTAs of a unit at least the last one sees every mark; if several
+// do, each combines the unit and writes the same bytes.  Who sees them all
+// clears them, for a replay of the call has the same nonce; a CTA that then
+// misses one leaves the unit to that one.
+__device__ __forceinline__ bool mark_done(unsigned long long* marks, unsigned long long nonce, int own, int first, int last,
+                                          int lane) {
+  if (lane == 0) {
+    __threadfence();
+    *static_cast<volatile unsigned long long*>(marks + own) = nonce;
+  }
+  __syncwarp();
+  __threadfence();
+  bool all = true;
+#pragma unroll 1
+  for (int c = first + lane; c <= last; c += 32) {
+    unsigned long long x;     // the first piece is in its CTA's second slot, the others in the first
+    asm volatile("ld.acquire.gpu.u64 %0, [%1];" : "=l"(x) : "l"(marks + 2 * c + (c == first)) : "memory");
+    all = all && x == nonce;
+  }
+  if (!__all_sync(0xffffffffu, all)) return false;
+#pragma unroll 1
+  for (int c = first + lane; c <= last; c += 32) *static_cast<volatile unsigned long long*>(marks + 2 * c + (c == first)) = 0;
+  return true;
+}
+
+// O = sum_s exp(LSE_s - LSE) O_s with LSE = log sum_s exp(LSE_s) over a unit's
+// pieces, a warp per row, the pieces in order (the same sum whichever CTA came
+// last).  Runs once, when its code is in no cache yet: the pieces come into the
+// ring's memory by bulk copies, as many at a time as fit, and are then added in
+// short loops.
+template <int D, int R>
+__device__ __forceinline__ void merge_unit(const PagedArgs& a, const Merge& u, uint8_t* ring, uint64_t* bar, uint32_t& phase,
+                                           const WaitCtx& wc) {
+  using S = PgShape<D, R>;
+  constexpr int kVec = D / 32;                       // columns per lane
+  constexpr int kRing = S::kNS * S::kStageBytes + 2 * S::kPBytes;
+  constexpr int kLse = kPagedCtas * R * 4;           // every piece's LSE comes first
+  constexpr int kBatch = (kRing - kLse) / (R * D * 4);
+  static_assert(kBatch >= 8, "pieces at a time");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hk = kv_head(a, u.unit);
+  const int row0 = (u.unit - hk * a.row_tiles) * R;
+  const int rows = min(R, a.rows - row0);
+  const int ns = u.last - u.first + 1;
+  const float* lse_s = reinterpret_cast<const float*>(ring);
+  const float* o_s = reinterpret_cast<const float*>(ring + kLse);
+  float m[R / 8 > 2 ? 2 : 1], L[R / 8 > 2 ? 2 : 1], acc[R / 8 > 2 ? 2 : 1][kVec];   // rows warp and warp + 16
+  constexpr int kRows = R / 8 > 2 ? 2 : 1;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    m[k] = -INFINITY;
+    L[k] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) acc[k][c] = 0.0f;
+  }
+  for (int s0 = 0; s0 < ns; s0 += kBatch) {
+    const int n = min(kBatch, ns - s0);
+    if (warp == 0) {
+      fence_proxy_async_all();
+      if (lane == 0) mbar_arrive_expect_tx(bar, n * rows * D * 4 + (s0 == 0 ? ns * R * 4 : 0));
+      __syncwarp();
+#pragma unroll 1
+      for (int s = lane; s < (s0 == 0 ? ns : n); s += 32) {
+        // the first piece is in its CTA's second slot, the others in the first
+        if (s0 == 0)
+          bulk_load(ring + s * (R * 4), a.part_lse + static_cast<size_t>(2 * (u.first + s) + (s == 0)) * R, R * 4, bar);
+        if (s < n)
+          bulk_load(ring + kLse + s * (R * D * 4),
+                    a.part_o + static_cast<size_t>(2 * (u.first + s0 + s) + (s0 + s == 0)) * (R * D), rows * D * 4, bar);
+      }
+    }
+    (void)pg_wait(bar, phase, wc, WAIT_PAGED_MERGE);    // if it runs out, the sums mean nothing
+    phase ^= 1u;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int r = warp + 16 * k;
+      if (r >= rows) break;
+      if (s0 == 0)
+#pragma unroll 1
+        for (int s = 0; s < ns; ++s) m[k] = fmaxf(m[k], lse_s[s * R + r]);
+#pragma unroll 1
+      for (int s = 0; s < n; ++s) {
+        const float x = lse_s[(s0 + s) * R + r];
+        const float w = x == -INFINITY ? 0.0f : ex2_approx((x - m[k]) * kLog2e);
+        L[k] += w;
+        const float* o = o_s + (s * R + r) * D + lane * kVec;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) acc[k][c] = fmaf(w, o[c], acc[k][c]);
+      }
+    }
+    __syncthreads();                                 // the ring is read: the next batch or unit may come
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = warp + 16 * k;
+    if (r >= rows) break;
+    const float inv = L[k] == 0.0f ? 0.0f : 1.0f / L[k];
+    const size_t out = (static_cast<size_t>(u.b) * a.Hkv + hk) * a.rows + row0 + r;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + out * D + lane * kVec);
+#pragma unroll
+    for (int c = 0; c < kVec; c += 2) dst[c / 2] = pack_bf16x2(acc[k][c] * inv, acc[k][c + 1] * inv);
+    if (lane == 0) a.lse[out] = L[k] == 0.0f ? -INFINITY : m[k] + log2f(L[k]) * kLn2;
+  }
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(kPgThreads, 1)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -365,7 +483,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(&b->o_free[lane], 4);
       mbar_init(&b->stats_full[lane], 8);
     }
-    if (lane == 0) b->abort = 0u;
+    if (lane == 0) {
+      mbar_init(&b->merged, 1);
+      b->abort = 0u;
+    }
     fence_mbar_init();
   } else if (warp >= 12) {
     for (int i = threadIdx.x - 384; i < 256; i += 128) b->nan_keys[i >> 7][i & 127] = 0u;
@@ -375,51 +496,49 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       *reinterpret_cast<uint4*>(sP + (i >> 6) * S::kPSub + 24 * 128 + (i & 63) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
-  // What came before in the stream may have written any of the inputs; the
-  // merge may be set up while this kernel runs.
+  // What came before in the stream may have written any of the inputs.
   grid_dependency_wait();
-  grid_dependency_launch();
   // This CTA's share of all tiles, and the place where it begins.  Tiles of one
   // KV head are summed in 32 bits (there are fewer than table entries).
-  const int chunk = (a.B + kPgThreads - 1) / kPgThreads;
-  const int c0 = min(a.B, static_cast<int>(threadIdx.x) * chunk), c1 = min(a.B, c0 + chunk);
-  unsigned mine = 0;
-  for (int i = c0; i < c1; ++i) mine += (pg_len(a, i) + TILE - 1) / TILE;
-  unsigned upto = mine;
+  if (warp == 0) {
+    const int chunk = (a.B + 31) >> 5;
+    const int c0 = min(a.B, lane * chunk), c1 = min(a.B, c0 + chunk);
+    unsigned mine = 0;
+#pragma unroll 4
+    for (int i = c0; i < c1; ++i) mine += (pg_len(a, i) + TILE - 1) / TILE;
+    unsigned upto = mine;
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const unsigned y = __shfl_up_sync(0xffffffffu, upto, m);
-    if (lane >= m) upto += y;
-  }
-  if (lane == 31) b->scan[warp] = upto;
-  __syncthreads();
-  unsigned before = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kPgThreads / 32; ++w) {
-    const unsigned x = b->scan[w];
-    if (w < warp) before += x;
-    sum += x;
-  }
-  const long long total = static_cast<long long>(sum) * a.units;
-  const int per = static_cast<int>((static_cast<unsigned long long>(total) + kPagedCtas - 1) / kPagedCtas);
-  const long long g0 = min(total, static_cast<long long>(blockIdx.x) * per);
-  const int n_tiles = static_cast<int>(min(total - g0, static_cast<long long>(per)));
-  long long first = static_cast<long long>(before + upto - mine) * a.units;
-  if (n_tiles > 0 && first <= g0 && g0 < first + static_cast<long long>(mine) * a.units) {
-    int i = c0, len = pg_len(a, c0), nt = (len + TILE - 1) / TILE;
-    while (g0 >= first + static_cast<long long>(nt) * a.units) {
-      first += static_cast<long long>(nt) * a.units;
-      len = pg_len(a, ++i);
-      nt = (len + TILE - 1) / TILE;
+    for (int m = 1; m < 32; m <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, upto, m);
+      if (lane >= m) upto += y;
     }
-    const unsigned pos = static_cast<unsigned>(g0 - first), unit = pos / static_cast<unsigned>(nt);
-    b->start = Place{i, static_cast<int>(unit), static_cast<int>(pos - unit * nt), len, nt};
+    const long long total = static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * a.units;
+    const int per = static_cast<int>((static_cast<unsigned long long>(total) + kPagedCtas - 1) / kPagedCtas);
+    const long long g0 = min(total, static_cast<long long>(blockIdx.x) * per);
+    const int n = static_cast<int>(min(total - g0, static_cast<long long>(per)));
+    long long first = static_cast<long long>(upto - mine) * a.units;
+    if (n > 0 && first <= g0 && g0 < first + static_cast<long long>(mine) * a.units) {
+      int i = c0, len = pg_len(a, c0), nt = (len + TILE - 1) / TILE;
+      while (g0 >= first + static_cast<long long>(nt) * a.units) {
+        first += static_cast<long long>(nt) * a.units;
+        len = pg_len(a, ++i);
+        nt = (len + TILE - 1) / TILE;
+      }
+      const unsigned pos = static_cast<unsigned>(g0 - first), unit = pos / static_cast<unsigned>(nt);
+      b->start = Place{i, static_cast<int>(unit), static_cast<int>(pos - unit * nt), len, nt};
+    }
+    if (lane == 0) {
+      b->per = per;
+      b->n_tiles = n;
+      b->n_merge = 0;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = b->tmem_base;
   const Place start = b->start;
+  const int per = b->per, n_tiles = b->n_tiles;
 
   if (n_tiles == 0) {
     // nothing but the empty requests below
@@ -783,25 +902,21 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // O^T row (= output column) held by this thread: M = d = 128 uses every
     // lane; M = 64 puts rows 16w..16w+15 in lanes 0-15 of quarter w.
     const int drow = (D == 128) ? wq * 32 + lane : (lane < 16 ? wq * 16 + lane : -1);
-    PagedNote note{-1, 0, 0, 0};
     Walk<TILE> walk(a, start, n_tiles);
     Piece pc;
+    bool ok = true;          // as for the softmax warps, for the barrier of cut pieces
     for (int it = 0; walk.next(pc); ++it) {
       const int ob = it & 1;
-      if (!pg_wait(&b->stats_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_STATS)) break;
+      ok = ok && pg_wait(&b->stats_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_STATS);
       const bool whole = pc.n == pc.nt;
       const int slot = 2 * blockIdx.x + (pc.j0 > 0 ? 0 : 1);
-      // a unit that an earlier CTA began is this CTA's first piece: it began
-      // ceil(j0 / per) shares before
-      if (pc.j0 > 0 && pc.j0 + pc.n == pc.nt)
-        note = PagedNote{pc.b, pc.unit, static_cast<int>(blockIdx.x) - (pc.j0 + per - 1) / per, 0};
       const int hk = kv_head(a, pc.unit);
       const int row0 = (pc.unit - hk * a.row_tiles) * R;
       const int rows = min(R, a.rows - row0);
       const size_t out = (static_cast<size_t>(pc.b) * a.Hkv + hk) * a.rows + row0;
       // lane r has row r's sum
       float inv = 0.0f;
-      if (lane < rows) {
+      if (ok && lane < rows) {
         const float L = b->stat_l[ob][0][lane] + b->stat_l[ob][1][lane] + b->stat_l[ob][2][lane] + b->stat_l[ob][3][lane];
         inv = L == 0.0f ? 0.0f : (1.0f / kBase) / L;
         if (wq == 0) {
@@ -812,7 +927,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             a.part_lse[slot * R + lane] = lse;
         }
       }
-      if (!pg_wait(&b->o_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_O)) break;
+      ok = ok && pg_wait(&b->o_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_O);
       tc_fence_after();
       const uint32_t bad = drow >= 0 ? b->nan_keys[ob][drow] : 0u;
       constexpr int kStep = R == 8 ? 8 : 16;
@@ -852,7 +967,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             i = i + 1 == a.Nq ? 0 : i + 1;
           }
         }
-        if (drow >= 0) {
+        if (ok && drow >= 0) {
           if (whole) {
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (out + rg) * D + drow;
 #pragma unroll
@@ -869,11 +984,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       if (bad != 0u) b->nan_keys[ob][drow] = 0u;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b->o_free[ob]);
+      if (ok && lane == 0) mbar_arrive(&b->o_free[ob]);
+      if (!whole) {
+        // the unit's CTAs: each has per tiles, so the first began ceil(j0 / per) shares before
+        const int c0 = static_cast<int>(blockIdx.x) - (pc.j0 + per - 1) / per;
+        const int c1 = static_cast<int>(blockIdx.x) + (pc.nt - pc.j0 - pc.n + per - 1) / per;
+        group_sync(3);
+        if (ok && warp == 12 && mark_done(a.marks, a.nonce, slot, c0, c1, lane) && lane == 0)
+          b->merge[b->n_merge++] = Merge{pc.b, pc.unit, c0, c1};
+      }
     }
-    if (threadIdx.x == 384) a.notes[blockIdx.x] = note;
   }
-  if (n_tiles == 0 && threadIdx.x == 384) a.notes[blockIdx.x] = PagedNote{-1, 0, 0, 0};
   // requests without a token
   if (warp >= 12) {
     const int t = threadIdx.x - 384;
@@ -892,58 +1013,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
-}
-
-// O = sum_s exp(LSE_s - LSE) O_s with LSE = log sum_s exp(LSE_s) over the
-// pieces of a unit that CTA blockIdx.x ended: its own and those of the CTAs
-// before it down to the one that began it.  A warp per row; the pieces are
-// added in order.
-constexpr int kMergeThreads = 256;
-
-template <int D, int R>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a) {
-  constexpr int kVec = D / 32;                       // columns per lane
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);   // row of the unit
-  grid_dependency_wait();
-  const PagedNote note = a.notes[blockIdx.x];
-  if (note.b < 0) return;
-  const int hk = kv_head(a, note.unit);
-  const int row = (note.unit - hk * a.row_tiles) * R + r;
-  if (row >= a.rows) return;
-  const int ns = blockIdx.x - note.first + 1;
-  // the first piece is in its CTA's second slot, the others in the first
-  auto slot = [&](int s) { return static_cast<size_t>(2 * (note.first + s) + (s == 0 ? 1 : 0)) * R + r; };
-  float m = -INFINITY, L = 0.0f;
-  bool bad = false;                                  // NaN must not hide from the maximum
-  for (int s = lane; s < ns; s += 32) {
-    const float x = a.part_lse[slot(s)];
-    bad |= x != x;
-    m = fmaxf(m, x);
-  }
-  m = redux_max(m);
-  bad = __any_sync(0xffffffffu, bad);
-  float acc[kVec] = {};
-  if (m != -INFINITY) {
-#pragma unroll 8
-    for (int s = 0; s < ns; ++s) {
-      const size_t at = slot(s);
-      const float w = ex2_approx((a.part_lse[at] - m) * kLog2e);
-      L += w;
-#pragma unroll
-      for (int c = 0; c < kVec; c += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * kVec + c);
-        acc[c] = fmaf(w, x.x, acc[c]);
-        acc[c + 1] = fmaf(w, x.y, acc[c + 1]);
-      }
-    }
-  }
-  const float inv = bad ? NAN : L > 0.0f ? 1.0f / L : 0.0f;
-  const size_t out = (static_cast<size_t>(note.b) * a.Hkv + hk) * a.rows + row;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + out * D + lane * kVec);
-#pragma unroll
-  for (int c = 0; c < kVec; c += 2) dst[c / 2] = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
-  if (lane == 0) a.lse[out] = bad ? NAN : L > 0.0f ? m + log2f(L) * kLn2 : -INFINITY;
+  uint32_t phase = 0;
+  const int n_merge = b->n_merge;
+  for (int i = 0; i < n_merge; ++i) merge_unit<D, R>(a, b->merge[i], smem, &b->merged, phase, wc);
 }
 
 template <int D, int R>
@@ -951,13 +1023,17 @@ cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const P
   constexpr size_t smem = pg_smem_bytes<D, R>();
   static_assert(smem <= 227 * 1024, "shared memory budget");
   auto kern = decode_paged_kernel<D, R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  static std::atomic<unsigned long long> configured{0};       // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(paged_merge_kernel<D, R>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return e;
-  // Both kernels may be set up before the one ahead of them in the stream has
-  // ended; each waits for it before its first access to memory.
+  if (dev > 63 || !((configured.load(std::memory_order_acquire) >> dev) & 1u)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) configured.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  // The kernel may be set up before the one ahead of it in the stream has
+  // ended; it waits for that before its first access to memory.
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -968,12 +1044,7 @@ cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const P
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(kPagedCtas, ((a.rows < R ? a.rows : R) + 7) / 8);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, R>, a);
+  return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
 }
 
 }  // namespace

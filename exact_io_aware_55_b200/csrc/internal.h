@@ -68,6 +68,7 @@ enum WaitSite : uint32_t {
   WAIT_PAGED_S_FREE = 76,
   WAIT_PAGED_P = 77,
   WAIT_PAGED_PV = 78,
+  WAIT_PAGED_MERGE = 79,
   // sites that report a page or slot outside the cache
   WAIT_APPEND_SLOT = 80,
   WAIT_TABLES_BACK = 81,
@@ -244,9 +245,6 @@ cudaError_t launch_page_tables(const TableArgs& a, cudaStream_t stream);
 
 // Attention over the 8-bit paged cache (fa_decode_paged.cu).
 constexpr int kPagedCtas = 148;   // one per SM of a B200; more or fewer SMs only change how they are shared out
-struct PagedNote {     // a CTA ended unit (b, unit), which CTA `first` began (b < 0: it ended none that it did not begin)
-  int b, unit, first, pad;
-};
 struct PagedArgs {
   uint32_t* status;
   const void* q;            // bf16 [B, H, Nq, d]
@@ -258,7 +256,8 @@ struct PagedArgs {
   float* lse;               // [B, H, Nq]
   float* part_o;            // workspace: fp32 [2 * CTAs, row tile, d], pieces of units cut between CTAs
   float* part_lse;          // workspace: fp32 [2 * CTAs, row tile]
-  PagedNote* notes;         // workspace: [CTAs]
+  unsigned long long* marks;      // workspace: [2 * CTAs], the nonce where a piece is done
+  unsigned long long nonce;       // not 0, another one each call
   int B, Hkv, Nq;
   int rows;                 // query rows that share a KV head: H / Hkv * Nq
   int row_tiles;            // tiles of them
