@@ -746,7 +746,10 @@ fa_status fa_page_tables(const int* ctx_lens, const int* new_lens, int* free_pag
                          int N, int n_free, int max_pages, int page_size, void* stream) {
   if (B < 0 || N < 0 || n_free < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
   if (!page_ok(page_size)) return FA_ERR_UNSUPPORTED;
-  if (B > 65535 || static_cast<long long>(max_pages) * page_size > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  // lengths, and the pages that a batch asks for or gives back, are counted in 32 bits
+  if (B > 65535 || static_cast<long long>(max_pages) * page_size > (1ll << 30) ||
+      static_cast<long long>(B) * max_pages > 0x7fffffffll || static_cast<long long>(B) * N > 0x7fffffffll)
+    return FA_ERR_UNSUPPORTED;
   if (B == 0) return FA_OK;
   if (!ctx_lens || !new_lens || !free_head || !seq_lens || !free_head_out) return FA_ERR_INVALID_ARG;
   if ((N > 0 && (!slots || !positions)) || (n_free > 0 && !free_pages) || (max_pages > 0 && !block_table))
@@ -769,7 +772,8 @@ fa_status fa_cache_append_fp8(const void* k, const void* v, const int* slots, vo
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (!page_ok(page_size)) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Hkv > 65535 || static_cast<long long>(B) * N > 0x7fffffffll ||
-      !cache_fits(num_pages, Hkv, page_size))
+      !cache_fits(num_pages, Hkv, page_size) ||
+      static_cast<long long>(B) * ((static_cast<long long>(N) + 15) / 16) * Hkv * 2 > 0x7fffffffll)   // blocks
     return FA_ERR_UNSUPPORTED;
   if (B == 0 || Hkv == 0 || N == 0) return FA_OK;
   if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return FA_ERR_INVALID_ARG;

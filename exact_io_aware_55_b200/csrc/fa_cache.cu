@@ -31,20 +31,23 @@ namespace fa {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kMaxWindow = 128;       // tokens whose runs one block looks for
 
-// Eight bf16 values times `inv` -> eight e4m3 codes; a value that is not finite
-// becomes the type's NaN.
-__device__ __forceinline__ uint2 quantise8(uint4 x, float inv) {
+// Eight bf16 values times `inv` -> eight e4m3 codes.  With `odd`, a value that is
+// not finite becomes the type's NaN (the conversion alone makes the largest
+// value of an infinity).
+__device__ __forceinline__ uint2 quantise8(uint4 x, float inv, bool odd) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t r[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(w[i] << 16) * inv, hi = __uint_as_float(w[i] & 0xffff0000u) * inv;
-    r[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-    if ((w[i] & 0x7f80u) == 0x7f80u) r[i] = (r[i] & 0xff00u) | 0x7fu;
-    if ((w[i] & 0x7f800000u) == 0x7f800000u) r[i] = (r[i] & 0x00ffu) | 0x7f00u;
-  }
+  for (int i = 0; i < 4; ++i)
+    r[i] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv),
+                                    __NV_SATFINITE, __NV_E4M3);
+  if (odd)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((w[i] & 0x7f80u) == 0x7f80u) r[i] = (r[i] & 0xff00u) | 0x7fu;
+      if ((w[i] & 0x7f800000u) == 0x7f800000u) r[i] = (r[i] & 0x00ffu) | 0x7f00u;
+    }
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
@@ -66,10 +69,14 @@ __device__ __forceinline__ uint2 rescale8(uint2 x, float ratio) {
   return make_uint2(w[0], w[1]);
 }
 
-// Largest absolute value among the finite ones of two packed bf16, as bits.
-__device__ __forceinline__ uint32_t amax_bits(uint32_t w) {
-  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
-  return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
+// Largest absolute values of the lower and the upper halves of bf16 pairs, as bits.
+__device__ __forceinline__ uint32_t amax2(uint4 x) {
+  constexpr uint32_t m = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
+}
+// Bits of a pair with what is not finite made 0.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0x7fffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0x7fff0000u);
 }
 
 // Power of two 2^e with the smallest e in [-60, 60] such that amax <= 448 * 2^e.
@@ -80,270 +87,344 @@ __device__ __forceinline__ float scale_for(uint32_t bf16_bits) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// A group of kTpi threads holds a page of one head, K or V, and works alone: it
+// takes a window of PAGE tokens of one request, finds the tokens that begin a
+// run on a page (none, or one or two as a rule) and writes those pages.  Every
+// warp of the group looks at the slots by itself; the group meets only for the
+// maximum.
 template <int D, int PAGE>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
-  constexpr int kTpi = PAGE * D / 64;                  // threads that hold a page
-  constexpr int kGroups = kAppendThreads / kTpi;
-  constexpr int kRowChunks = D / 8;                    // 16-byte groups of a row
-  __shared__ int s_lead[kMaxWindow];
-  __shared__ int s_count;
-  __shared__ int s_src[kGroups][PAGE];
-  __shared__ int s_stop[kGroups];
+struct AppendShape {
+  static constexpr int kTpi = PAGE * D / 64 > 32 ? PAGE * D / 64 : 32;
+  static constexpr int kChunks = PAGE * D / 8 / kTpi;  // 16-byte groups of eight elements per thread
+  static constexpr int kGroups = kAppendThreads / kTpi;
+};
+
+template <int D, int PAGE>
+__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const AppendArgs a) {
+  using S = AppendShape<D, PAGE>;
+  constexpr int kTpi = S::kTpi, kChunks = S::kChunks;
+  constexpr int kRowChunks = D / 8;
+  __shared__ int s_slot[S::kGroups][2 * PAGE];
+  __shared__ int s_src[S::kGroups][PAGE];
   __shared__ uint32_t s_max[kAppendThreads / 32];
-  const int b = blockIdx.x / a.windows;
-  const int n0 = (blockIdx.x - b * a.windows) * a.window;
-  const int n1 = min(a.N, n0 + a.window);
-  const int h0 = blockIdx.y * a.heads_per_block;
-  const int nh = min(a.Hkv - h0, a.heads_per_block);
-  const int* slots = a.slots + static_cast<long long>(b) * a.N;
-  const long long n_slots = static_cast<long long>(a.num_pages) * PAGE;
-  auto page_of = [&](int n) -> int {
-    const int s = slots[n];
-    return s >= 0 && s < n_slots ? s / PAGE : -1;
+  const int group = threadIdx.x / kTpi, t = threadIdx.x % kTpi, lane = threadIdx.x & 31;
+  auto meet = [&]() {        // the group's threads (ids 1.. of the hardware barriers)
+    if constexpr (kTpi == 32)
+      __syncwarp();
+    else
+      asm volatile("barrier.cta.sync %0, %1;" ::"r"(group + 1), "n"(kTpi) : "memory");
   };
-  if (threadIdx.x == 0) s_count = 0;
-  __syncthreads();
-  for (int n = n0 + threadIdx.x; n < n1; n += kAppendThreads) {
-    const int p = page_of(n);
-    if (slots[n] >= n_slots) report_status(a.status, DEVSTATUS_BAD_PAGE, WAIT_APPEND_SLOT);
-    if (p >= 0 && (n == 0 || page_of(n - 1) != p)) s_lead[atomicAdd(&s_count, 1)] = n;
-  }
-  __syncthreads();
-  const int group = threadIdx.x / kTpi, lane = threadIdx.x % kTpi;
-  const int items = s_count * nh * 2;
-  for (int first = 0; first < items; first += kGroups) {
-    const int item = first + group;
-    const bool active = item < items;
-    const int is_v = item & 1;
-    const int h = h0 + (active ? (item >> 1) % nh : 0);
-    const int lead = active ? s_lead[(item >> 1) / nh] : 0;
-    const int page = active ? page_of(lead) : 0;
-    // the token that each of the page's slots gets, from the run of tokens that
-    // starts at `lead` and stays on the page (the last one where two name a slot)
-    for (int i = lane; i < PAGE; i += kTpi) s_src[group][i] = -1;
-    if (lane == 0) s_stop[group] = a.N;
-    __syncthreads();
-    bool more = active;
-    for (int base = lead;; base += kTpi) {
-      const int n = base + lane;
-      const bool mine = more && n < a.N && page_of(n) == page;
-      if (more && !mine) atomicMin(&s_stop[group], n);
-      __syncthreads();
-      const int stop = s_stop[group];
-      if (mine && n < stop) atomicMax(&s_src[group][slots[n] % PAGE], n);
-      more = more && stop >= base + kTpi && base + kTpi < a.N;
-      if (!__syncthreads_or(more)) break;
-    }
-    const int* src = s_src[group];
-    const bool fresh = src[0] >= 0;
-    const long long ph = static_cast<long long>(page) * a.Hkv + h;
-    float* scale = (is_v ? a.v_scale : a.k_scale) + ph;
-    uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + ph * (PAGE * D);
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) +
-                             (static_cast<long long>(b) * a.Hkv + h) * a.N * D;
-    uint4 val[8];
-    uint32_t top = 0;
-    float was = 0.0f;
-    if (active) {
+  // (request, window, head, K or V), the last fastest: neighbours read the same slots
+  const unsigned item = blockIdx.x * S::kGroups + group;
+  const bool is_v = item & 1u;
+  const unsigned bwh = item >> 1, bw = bwh / static_cast<unsigned>(a.Hkv);
+  const int h = static_cast<int>(bwh - bw * a.Hkv);
+  const int b = static_cast<int>(bw / static_cast<unsigned>(a.windows));
+  const int n0 = static_cast<int>(bw - static_cast<unsigned>(b) * a.windows) * PAGE;
+  if (b >= a.B) return;
+  grid_dependency_wait();
+  const int* slots = a.slots + static_cast<long long>(b) * a.N;
+  const int n_slots = static_cast<int>(min(static_cast<long long>(a.num_pages) * PAGE, 0x7fffffffll));
+  auto fetch = [&](int n) {
+    const int s = n < a.N ? slots[n] : -1;
+    return s < n_slots ? s : -1;
+  };
+  // the window's slots and as many behind it; -1: none
+  int* near = s_slot[group];
+  int before = n0 > 0 && t == 0 ? fetch(n0 - 1) : -1;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = i * kTpi + lane;
-        const int n = src[c / kRowChunks];
+  for (int i = t; i < 2 * PAGE; i += kTpi) {
+    near[i] = fetch(n0 + i);
+    if (i < PAGE && n0 + i < a.N && slots[n0 + i] >= n_slots) report_status(a.status, DEVSTATUS_BAD_PAGE, WAIT_APPEND_SLOT);
+  }
+  meet();
+  if constexpr (kTpi > 32) {
+    if (t == 0) s_src[group][0] = before;
+    meet();
+    before = s_src[group][0];
+    meet();
+  } else {
+    before = __shfl_sync(0xffffffffu, before, 0);
+  }
+  auto slot_of = [&](int n) { return n - n0 < 2 * PAGE ? near[n - n0] : fetch(n); };   // n >= n0
+  const int n1 = min(a.N, n0 + PAGE);
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) +
+                           (static_cast<long long>(b) * a.Hkv + h) * a.N * D;
+#pragma unroll 1
+  for (int c0 = n0; c0 < n1; c0 += 32) {
+    const int mine = c0 + lane;
+    const int slot = mine < n1 ? near[mine - n0] : -1;
+    const int prev = mine == n0 ? before : mine < n1 ? near[mine - n0 - 1] : -1;
+    uint32_t leads = __ballot_sync(0xffffffffu, slot >= 0 && (prev < 0 || prev / PAGE != slot / PAGE));
+#pragma unroll 1
+    for (; leads != 0; leads &= leads - 1) {
+      const int lead = c0 + __ffs(leads) - 1;
+      const int first = __shfl_sync(0xffffffffu, slot, __ffs(leads) - 1);
+      const int page = first / PAGE, off = first - page * PAGE;
+      // tokens in a row on slots in a row, up to the page's end
+      int len = 0;
+#pragma unroll 1
+      for (;; len += 32) {
+        const int k = len + lane;
+        const uint32_t in = __ballot_sync(0xffffffffu, k < PAGE - off && near[lead - n0 + k] == first + k);
+        if (in != 0xffffffffu) {
+          len += __ffs(~in) - 1;
+          break;
+        }
+      }
+      // a run that goes on upon the page in another order: the later of two
+      // tokens of one slot is stored
+      const int behind = slot_of(lead + len);
+      const bool odd = behind >= 0 && behind / PAGE == page;
+      int* src = s_src[group];
+      if (odd) {
+        for (int i = t; i < PAGE; i += kTpi) src[i] = -1;
+        meet();
+#pragma unroll 1
+        for (int base = lead;; base += 32) {
+          const int q = slot_of(base + lane);
+          const uint32_t in = __ballot_sync(0xffffffffu, q >= 0 && q / PAGE == page);
+          const int n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+          if (lane < n) atomicMax(&src[q % PAGE], base + lane);
+          if (n < 32) break;
+        }
+        meet();
+      }
+      const bool fresh = odd ? src[0] >= 0 : off == 0;
+      const long long ph = static_cast<long long>(page) * a.Hkv + h;
+      float* scale = (is_v ? a.v_scale : a.k_scale) + ph;
+      uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + ph * (PAGE * D);
+      float was = fresh ? 0.0f : *scale;
+      uint4 val[kChunks];
+      uint32_t put = 0;
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = i * kTpi + t, row = c / kRowChunks;
+        const int n = odd ? src[row] : row >= off && row < off + len ? lead + row - off : -1;
+        if (n >= 0) put |= 1u << i;
         val[i] = n >= 0 ? *reinterpret_cast<const uint4*>(x + static_cast<long long>(n) * D + (c % kRowChunks) * 8)
                         : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (!fresh) was = *scale;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        top = max(max(top, max(amax_bits(val[i].x), amax_bits(val[i].y))), max(amax_bits(val[i].z), amax_bits(val[i].w)));
-    }
+      for (int i = 0; i < kChunks; ++i) top = __vmaxu2(top, amax2(val[i]));
+      bool strange = __any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u);
+      if (strange) {         // the finite ones alone
+        top = 0;
 #pragma unroll
-    for (int m = (kTpi < 32 ? kTpi : 32) / 2; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-    if (kTpi > 32) {
-      if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
-      __syncthreads();
-      constexpr int kWarps = kTpi > 32 ? kTpi / 32 : 1;
+        for (int i = 0; i < kChunks; ++i)
+          top = __vmaxu2(top, amax2(make_uint4(finite2(val[i].x), finite2(val[i].y), finite2(val[i].z), finite2(val[i].w))));
+      }
+      top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+      if constexpr (kTpi > 32) {
+        if (lane == 0) s_max[threadIdx.x >> 5] = top;
+        meet();
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = max(top, s_max[group * kWarps + w]);
-    }
-    if (active) {
+        for (int w = 0; w < kTpi / 32; ++w) top = max(top, s_max[group * (kTpi / 32) + w]);
+      }
       if (!(was > 0.0f && was <= 3.0e38f)) was = 0.0f;    // no usable scale: nothing of the page is kept
       const float now = fmaxf(was, scale_for(top));
       const float inv = 1.0f / now;
       const bool grow = !fresh && now != was;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = i * kTpi + lane;
-        uint2* p = reinterpret_cast<uint2*>(codes + c * 8);
-        if (src[c / kRowChunks] >= 0)
-          *p = quantise8(val[i], inv);
+      for (int i = 0; i < kChunks; ++i) {
+        uint2* p = reinterpret_cast<uint2*>(codes + (i * kTpi + t) * 8);
+        if ((put >> i) & 1u)
+          *p = quantise8(val[i], inv, strange);
         else if (grow)
           *p = was > 0.0f ? rescale8(*p, was * inv) : make_uint2(0u, 0u);
       }
-    }
-    __syncthreads();      // every thread has read the old scale and the slot map
-    if (active && lane == 0) {
-      if (!(was > 0.0f)) *scale = scale_for(top);
-      else *scale = fmaxf(was, scale_for(top));
+      meet();               // the old scale, the slot map and the maxima are read
+      if (t == 0) *scale = now;
     }
   }
 }
 
 template <int D, int PAGE>
 cudaError_t launch_append_t(AppendArgs a, cudaStream_t stream) {
-  constexpr int kGroups = kAppendThreads / (PAGE * D / 64);
-  constexpr int kHalf = kGroups > 1 ? kGroups / 2 : 1;
-  // a block has about kGroups pages of K and V: of several heads where there is
-  // one run of tokens, of several runs where there are many
-  a.heads_per_block = a.N <= PAGE ? kHalf : 1;
-  a.window = a.N <= PAGE ? a.N : PAGE * kHalf;
-  static_assert(PAGE * kHalf <= kMaxWindow, "window list");
-  a.windows = (a.N + a.window - 1) / a.window;
-  const dim3 grid(static_cast<unsigned>(a.B) * a.windows, (a.Hkv + a.heads_per_block - 1) / a.heads_per_block);
-  cache_append_kernel<D, PAGE><<<grid, kAppendThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  a.windows = (a.N + PAGE - 1) / PAGE;
+  const long long items = static_cast<long long>(a.B) * a.windows * a.Hkv * 2;
+  const long long blocks = (items + AppendShape<D, PAGE>::kGroups - 1) / AppendShape<D, PAGE>::kGroups;
+  return launch_dependent(cache_append_kernel<D, PAGE>, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0, stream, a);
 }
 
 // Page tables of a batch.  Request b holds ceil(ctx / P) pages and wants to
 // grow by new_lens[b] tokens, or (negative) has finished.  Pages of finished
 // requests go in front of the free ones; then requests take pages in order:
 // request b is granted when need = 0 or the needs up to and with b still fit.
-// Two prefix sums over the batch.  The blocks of one cluster each take the
-// sums in batches of kTabThreads requests, redundantly (the lengths are a few
-// kilobytes out of L2), and share the writing; the cluster barrier puts the
-// returned pages before their reuse and every read of an input before the
-// write of an output that may be the same memory.
+// Two prefix sums over the batch, taken together in the halves of one 64-bit
+// number.  The blocks of one cluster each take them redundantly, kTabThreads
+// requests at a time (the lengths are a few kilobytes out of L2), and share the
+// writing; the cluster barrier puts the returned pages before their reuse and
+// every read of an input before the write of an output that may be the same
+// memory.
 constexpr int kTabThreads = 1024;
 constexpr int kTabCluster = 8;
 
 struct TabRow {
-  int ctx, nw, held, start, need;      // nw < 0: not granted
+  int ctx, nw, held, start, need;      // nw < 0: no slots
 };
 
-// Inclusive prefix sum over the block; *total gets the sum.
-__device__ __forceinline__ long long block_scan(long long x, long long* s_warp, long long* total) {
+// Inclusive prefix sum over the block; `total` gets the sum.
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long x, unsigned long long* s_warp,
+                                                         unsigned long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, m);
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, m);
     if (lane >= m) x += y;
   }
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    long long w = s_warp[lane];
+  unsigned long long w = s_warp[lane];     // every warp scans the warps' sums
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, w, m);
-      if (lane >= m) w += y;
-    }
-    s_warp[lane] = w;
+  for (int m = 1; m < 32; m <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, w, m);
+    if (lane >= m) w += y;
   }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const unsigned long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   __syncthreads();
-  if (warp > 0) x += s_warp[warp - 1];
-  *total = s_warp[31];
-  __syncthreads();
-  return x;
+  return warp > 0 ? x + before : x;
 }
 
 __global__ void __launch_bounds__(kTabThreads) __cluster_dims__(kTabCluster, 1, 1) page_tables_kernel(const TableArgs a) {
   namespace cg = cooperative_groups;
   __shared__ TabRow s_row[kTabThreads];
-  __shared__ long long s_warp[32];
+  __shared__ unsigned long long s_warp[32];
+  __shared__ int s_taken;
   const auto cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
-  const int P = a.page;
-  const long long cap = static_cast<long long>(a.max_pages) * P;
+  const int warp = (threadIdx.x >> 5) + rank * (kTabThreads / 32), lane = threadIdx.x & 31;   // of the cluster
+  constexpr int kWarps = kTabCluster * kTabThreads / 32;
+  const int shift = 31 - __clz(a.page), P = a.page;
+  const int cap = a.max_pages << shift;
+  if (threadIdx.x == 0) s_taken = 0;
+  grid_dependency_wait();
   const int head = min(max(*a.free_head, 0), a.n_free);
-  auto ctx_of = [&](int b) { return static_cast<int>(min(static_cast<long long>(max(a.ctx_lens[b], 0)), cap)); };
-  // pages that come back, and their places in front of the free ones
-  long long back = 0;
+  const bool once = a.B <= kTabThreads;
+  TabRow row;
+  bool finished;
+  // request b's row before anything is granted; pages that come back in `back`
+  auto load = [&](int b, int& back) {
+    row = TabRow{0, -1, 0, 0, 0};
+    finished = false;
+    back = 0;
+    if (b >= a.B) return;
+    const int nw = a.new_lens[b];
+    row.ctx = min(max(a.ctx_lens[b], 0), cap);
+    row.held = (row.ctx + P - 1) >> shift;
+    finished = nw < 0;
+    if (finished) back = row.held;
+    if (nw >= 0 && nw <= a.N && nw <= cap - row.ctx) {
+      row.nw = nw;
+      row.need = ((row.ctx + nw + P - 1) >> shift) - row.held;
+    }
+  };
+  unsigned long long end = 0, total = 0, carry = 0;
+  int back;
   for (int base = 0; base < a.B; base += kTabThreads) {
-    const int b = base + threadIdx.x;
-    long long total;
-    block_scan(b < a.B && a.new_lens[b] < 0 ? (ctx_of(b) + P - 1) / P : 0, s_warp, &total);
-    back += total;
+    load(base + threadIdx.x, back);
+    end = block_scan((static_cast<unsigned long long>(back) << 32) | static_cast<unsigned>(row.need), s_warp, total);
+    carry += total >> 32;
   }
-  const bool fits = back <= head;            // else the caller's lists contradict each other: nothing comes back
-  if (!fits && rank == 0 && threadIdx.x == 0) report_status(a.status, DEVSTATUS_BAD_PAGE, WAIT_TABLES_BACK);
-  const int low = fits ? static_cast<int>(head - back) : head;
-  if (fits && back > 0) {
-    long long carry = 0;
+  const bool fits = carry <= static_cast<unsigned long long>(head);
+  if (!fits && warp == 0 && lane == 0) report_status(a.status, DEVSTATUS_BAD_PAGE, WAIT_TABLES_BACK);
+  const int low = fits ? head - static_cast<int>(carry) : head;   // else the lists contradict each other: nothing comes back
+  if (fits && carry > 0) {
+    int start = 0;
     for (int base = 0; base < a.B; base += kTabThreads) {
-      const int b = base + threadIdx.x;
-      const int held = b < a.B && a.new_lens[b] < 0 ? (ctx_of(b) + P - 1) / P : 0;
-      long long total;
-      const long long end = block_scan(held, s_warp, &total) + carry;
-      s_row[threadIdx.x] = TabRow{0, 0, held, static_cast<int>(end - held), 0};
+      if (!once) {
+        load(base + threadIdx.x, back);
+        end = block_scan(static_cast<unsigned long long>(back) << 32, s_warp, total);
+      }
+      s_row[threadIdx.x] = TabRow{0, 0, back, start + static_cast<int>(end >> 32) - back, 0};
+      start += static_cast<int>(total >> 32);
       __syncthreads();
       const int rows = min(kTabThreads, a.B - base);
-      for (int r = rank * 32 + (threadIdx.x >> 5); r < rows; r += kTabCluster * 32)
-        for (int i = threadIdx.x & 31; i < s_row[r].held; i += 32)
-          a.free_pages[low + s_row[r].start + i] =
-              a.block_table[static_cast<long long>(base + r) * a.max_pages + i];
-      carry += total;
+#pragma unroll 1
+      for (int r = warp; r < rows; r += kWarps)
+#pragma unroll 4
+        for (int i = lane; i < s_row[r].held; i += 32)
+          a.free_pages[low + s_row[r].start + i] = a.block_table[static_cast<long long>(base + r) * a.max_pages + i];
       __syncthreads();
     }
   }
   cluster.sync();
-  const long long avail = a.n_free - low;
-  long long carry = 0;
-  int taken = 0;
+  const unsigned avail = a.n_free - low;
+  unsigned asked = 0;                    // by the requests of the batches before
   for (int base = 0; base < a.B; base += kTabThreads) {
-    const int b = base + threadIdx.x;
-    TabRow row{0, -1, 0, 0, 0};
-    bool finished = false;
-    if (b < a.B) {
-      const int nw = a.new_lens[b];
-      row.ctx = ctx_of(b);
-      row.held = (row.ctx + P - 1) / P;
-      finished = nw < 0;
-      if (nw >= 0 && nw <= a.N && row.ctx + static_cast<long long>(nw) <= cap) {
-        row.nw = nw;
-        row.need = (row.ctx + nw + P - 1) / P - row.held;
+    if (!once) {
+      load(base + threadIdx.x, back);
+      end = block_scan(static_cast<unsigned>(row.need), s_warp, total);
+      // another block may still read the lengths that are about to be overwritten
+      cluster.sync();
+    }
+    const unsigned upto = asked + static_cast<unsigned>(end);
+    asked += static_cast<unsigned>(total);
+    if (row.need > 0) {
+      if (upto > avail) {
+        row.nw = -1;
+        row.need = 0;
+      } else {
+        row.start = low + static_cast<int>(upto) - row.need;
+        // needs only add up, so the granted ones come first: what they take is the last's sum
+        if (asked > avail) atomicMax(&s_taken, static_cast<int>(upto));
       }
     }
-    long long total;
-    const long long end = block_scan(row.need, s_warp, &total) + carry;
-    if (row.need > 0 && end > avail) {
-      row.nw = -1;
-      row.need = 0;
-    }
-    row.start = static_cast<int>(min(end - row.need, static_cast<long long>(a.n_free)));
-    carry += total;
-    // the needs' sums never fall, so what is granted is the largest sum that fits
-    long long granted;
-    block_scan(row.need, s_warp, &granted);
-    taken += static_cast<int>(granted);
     s_row[threadIdx.x] = row;
-    // another block may still read the lengths that are about to be overwritten
-    cluster.sync();
+    const int b = base + threadIdx.x;
     if (b < a.B && rank == 0) a.seq_lens[b] = finished ? 0 : row.ctx + max(row.nw, 0);
+    if (asked <= avail && threadIdx.x == 0) s_taken = static_cast<int>(asked);
+    __syncthreads();
     const int rows = min(kTabThreads, a.B - base);
-    for (int r = rank * 32 + (threadIdx.x >> 5); r < rows; r += kTabCluster * 32)
-      for (int i = threadIdx.x & 31; i < s_row[r].need; i += 32)
-        a.block_table[static_cast<long long>(base + r) * a.max_pages + s_row[r].held + i] =
-            a.free_pages[low + s_row[r].start + i];
-    const long long cells = static_cast<long long>(rows) * a.N;
-    for (long long i = rank * kTabThreads + threadIdx.x; i < cells; i += kTabCluster * kTabThreads) {
-      const int r = static_cast<int>(i / a.N);
-      const int t = static_cast<int>(i - static_cast<long long>(r) * a.N);
-      const TabRow w = s_row[r];
-      int slot = -1, pos = 0;
-      if (t < w.nw) {
-        pos = w.ctx + t;
-        const int lp = pos / P;
-        const int page = lp < w.held ? a.block_table[static_cast<long long>(base + r) * a.max_pages + lp]
-                                     : a.free_pages[low + w.start + lp - w.held];
-        if (page >= 0 && page < 0x7fffffff / P) slot = page * P + (pos - lp * P);
+    // Slot of new token t; the first one on a new page enters it in the table.
+    auto slot = [&](const TabRow& w, int r, int t, int& pos) {
+      pos = 0;
+      if (t >= w.nw) return -1;
+      pos = w.ctx + t;
+      const int lp = pos >> shift;
+      int* entry = a.block_table + static_cast<long long>(base + r) * a.max_pages + lp;
+      const int page = lp < w.held ? *entry : a.free_pages[w.start + lp - w.held];
+      if (lp >= w.held && (pos & (P - 1)) == 0) *entry = page;
+      return page >= 0 && page < 0x7fffffff / P ? (page << shift) + (pos & (P - 1)) : -1;
+    };
+    if (a.N >= 32) {           // a warp takes 128 tokens of a request
+      const unsigned parts = (static_cast<unsigned>(a.N) + 127) >> 7;
+      const unsigned long long items = static_cast<unsigned long long>(parts) * rows;
+      unsigned r = warp / parts, part = warp - r * parts;
+#pragma unroll 1
+      for (unsigned long long i = warp; i < items; i += kWarps) {
+        const TabRow w = s_row[r];
+        const long long at = static_cast<long long>(base + r) * a.N;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int t = static_cast<int>(part * 128 + k * 32) + lane;
+          if (t < a.N) {
+            int pos;
+            a.slots[at + t] = slot(w, r, t, pos);
+            a.positions[at + t] = pos;
+          }
+        }
+        part += kWarps;
+        const unsigned over = part / parts;
+        r += over;
+        part -= over * parts;
       }
-      const long long at = static_cast<long long>(base) * a.N + i;
-      a.slots[at] = slot;
-      a.positions[at] = pos;
+    } else {
+      const unsigned cells = static_cast<unsigned>(rows) * a.N;
+#pragma unroll 1
+      for (unsigned i = rank * kTabThreads + threadIdx.x; i < cells; i += kTabCluster * kTabThreads) {
+        const unsigned r = i / static_cast<unsigned>(a.N);
+        int pos;
+        const long long at = static_cast<long long>(base) * a.N + i;
+        a.slots[at] = slot(s_row[r], r, i - r * a.N, pos);
+        a.positions[at] = pos;
+      }
     }
     __syncthreads();
   }
-  if (rank == 0 && threadIdx.x == 0) *a.free_head_out = low + taken;
+  if (rank == 0 && threadIdx.x == 0) *a.free_head_out = low + s_taken;
 }
 
 }  // namespace
@@ -366,8 +447,7 @@ cudaError_t launch_cache_append(const AppendArgs& a, int d, cudaStream_t stream)
 }
 
 cudaError_t launch_page_tables(const TableArgs& a, cudaStream_t stream) {
-  page_tables_kernel<<<kTabCluster, kTabThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(page_tables_kernel, dim3(kTabCluster), dim3(kTabThreads), 0, stream, a);
 }
 
 }  // namespace fa

@@ -176,9 +176,6 @@ __device__ __forceinline__ bool pg_wait3(uint64_t* x, uint32_t px, uint64_t* y, 
          (pg_wait_slow(x, px, w, where) && pg_wait_slow(y, py, w, where) && pg_wait_slow(z, pz, w, where));
 }
 
-// Programmatic dependent launch: wait for the grids before this one in the stream.
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // N (4, 8, 16) consecutive TMEM columns of this thread's lane.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[N]) {
@@ -1032,19 +1029,7 @@ cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const P
     if (e != cudaSuccess) return e;
     if (dev <= 63) configured.fetch_or(1ull << dev, std::memory_order_release);
   }
-  // The kernel may be set up before the one ahead of it in the stream has
-  // ended; it waits for that before its first access to memory.
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kPagedCtas);
-  cfg.blockDim = dim3(kPgThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+  return launch_dependent(kern, dim3(kPagedCtas), dim3(kPgThreads), smem, stream, tk, tv, a);
 }
 
 }  // namespace

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace fa {
 
@@ -76,6 +77,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   const int n = static_cast<int>(token - static_cast<long long>(b) * a.N);
   const int turned = a.rot_dim >> 4;                 // chunks that are turned
   const bool turns = chunk < turned;
+  grid_dependency_wait();
   if (!turns && a.in_place) return;
   int ou, ow;                                        // element offsets of the two 8-element groups
   if (INTERLEAVED || !turns) {
@@ -116,15 +118,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 cudaError_t launch_rope(RopeArgs a, bool interleaved, cudaStream_t stream) {
   const long long threads = static_cast<long long>(a.B) * a.N * (a.d >> 4);
   a.heads_per_thread = 8;
-  while (a.heads_per_thread > 1 && threads * ((a.H + a.heads_per_thread - 1) / a.heads_per_thread) < 148ll * 2048)
+  while (a.heads_per_thread > 1 && threads * ((a.H + a.heads_per_thread - 1) / a.heads_per_thread) < 148ll * 1024)
     a.heads_per_thread >>= 1;
   const dim3 grid(static_cast<unsigned>((threads + kRopeThreads - 1) / kRopeThreads),
                   static_cast<unsigned>((a.H + a.heads_per_thread - 1) / a.heads_per_thread));
-  if (interleaved)
-    rope_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a);
-  else
-    rope_kernel<false><<<grid, kRopeThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(interleaved ? rope_kernel<true> : rope_kernel<false>, grid, dim3(kRopeThreads), 0, stream, a);
 }
 
 }  // namespace fa

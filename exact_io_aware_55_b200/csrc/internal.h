@@ -194,6 +194,24 @@ template <int D, bool CAUSAL>
 cudaError_t launch_bwd_dq(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
 
+// Launches a kernel that may be set up before the one ahead of it in the stream
+// has ended; it calls grid_dependency_wait() before its first access to memory.
+template <typename Kernel, typename... Args>
+cudaError_t launch_dependent(Kernel kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Rotary positions on [B, H, N, d] bf16 (fa_rope.cu).
 struct RopeArgs {
   const void* x;
@@ -223,7 +241,7 @@ struct AppendArgs {
   int B, Hkv, N;
   int num_pages;
   int page;
-  int window, windows, heads_per_block;   // set by the launcher
+  int windows;         // of `page` tokens per request; set by the launcher
 };
 cudaError_t launch_cache_append(const AppendArgs& a, int d, cudaStream_t stream);
 
