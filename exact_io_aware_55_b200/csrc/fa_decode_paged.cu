@@ -39,8 +39,8 @@
 // results do not depend on timing.
 //
 // Warps: 0 page ids and TMA, 1 MMA issuer and TMEM owner, 2 page scales,
-// 3 queries, 4-7 and 8-11 softmax (thread = key, each group half of the rows;
-// TMEM lane quarter = warp % 4), 12-15 epilogue.  Pages that lie behind the length or outside the cache are not
+// 3 queries, from 4 on the softmax groups of four (thread = key, each group its
+// share of the rows; TMEM lane quarter = warp % 4), the last four epilogue.  Pages that lie behind the length or outside the cache are not
 // loaded; the softmax warps clear the V rows of keys that are not there, since
 // p = 0 times a stale NaN code would be NaN.
 #include <cuda_bf16.h>
@@ -56,13 +56,16 @@ namespace fa {
 
 namespace {
 
-constexpr int kPgThreads = 512;
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
 constexpr float kBase = 1024.0f;            // P is scaled by 2^10: below 2^15, of e5m2's 57344
 
 template <int D, int R>
 struct PgShape {
+  static constexpr int kGroups = R == 32 ? 4 : 2;             // of softmax warps
+  static constexpr int kRows = R / kGroups;                   // rows of each
+  static constexpr int kEpi = 4 + 4 * kGroups;                // first epilogue warp
+  static constexpr int kThreads = 32 * (kEpi + 4);
   static constexpr int kSub = (D == 64) ? 2 : 1;              // 128-key sub-tiles per tile
   static constexpr int kTileKeys = 128 * kSub;
   static constexpr int kTileBytes = kTileKeys * D;            // K (or V) codes of one tile
@@ -238,21 +241,21 @@ __device__ __forceinline__ void split_pair(uint32_t q, float inv, uint32_t& hi, 
 
 __device__ __forceinline__ int pg_len(const PagedArgs& a, int b) { return min(max(a.seq_lens[b], 0), a.max_pages * a.page); }
 
-// Clears the NaN codes (0x7f, 0xff) in one half of row `kt` of a V tile and sets
+// Clears the NaN codes (0x7f, 0xff) in part `part` of row `kt` of a V tile and sets
 // bit `edge` for their columns; the flags of the piece two before are the
 // epilogue's until it frees them.
-template <int D>
-__device__ __noinline__ bool clear_nan_codes(uint8_t* v, int kt, int half, int edge, uint32_t* nan_keys,
+template <int D, int PARTS>
+__device__ __noinline__ bool clear_nan_codes(uint8_t* v, int kt, int part, int edge, uint32_t* nan_keys,
                                              uint64_t* o_free, int it, bool ok, const WaitCtx& wc) {
-  uint32_t* row = reinterpret_cast<uint32_t*>(v + kt * D + half * (D / 2));
+  uint32_t* row = reinterpret_cast<uint32_t*>(v + kt * D + part * (D / PARTS));
   bool waited = it < 2;
-  for (int c = 0; c < D / 8; ++c) {
+  for (int c = 0; c < D / PARTS / 4; ++c) {
     const uint32_t x = row[c], bad = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
     if (bad == 0u) continue;
     if (!waited) ok = ok && mbar_wait(o_free, ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE);
     waited = true;
     row[c] = x & ~bad;
-    const int byte = half * (D / 2) + c * 4;                       // place in the swizzled row
+    const int byte = part * (D / PARTS) + c * 4;                       // place in the swizzled row
     const int unit = (byte >> 4) ^ (D == 128 ? kt & 7 : (kt >> 1) & 3);
     for (int k = 0; k < 4; ++k)
       if ((bad >> (8 * k)) & 1u) atomicOr(&nan_keys[unit * 16 + (byte & 15) + k], 1u << edge);
@@ -383,8 +386,8 @@ __device__ __forceinline__ void merge_unit(const PagedArgs& a, const Merge& u, u
   const int ns = u.last - u.first + 1;
   const float* lse_s = reinterpret_cast<const float*>(ring);
   const float* o_s = reinterpret_cast<const float*>(ring + kLse);
-  float m[R / 8 > 2 ? 2 : 1], L[R / 8 > 2 ? 2 : 1], acc[R / 8 > 2 ? 2 : 1][kVec];   // rows warp and warp + 16
-  constexpr int kRows = R / 8 > 2 ? 2 : 1;
+  constexpr int kWarps = S::kThreads / 32, kRows = (R + kWarps - 1) / kWarps;
+  float m[kRows], L[kRows], acc[kRows][kVec];        // of rows warp, warp + kWarps
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     m[k] = -INFINITY;
@@ -412,7 +415,7 @@ __device__ __forceinline__ void merge_unit(const PagedArgs& a, const Merge& u, u
     phase ^= 1u;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-      const int r = warp + 16 * k;
+      const int r = warp + kWarps * k;
       if (r >= rows) break;
       if (s0 == 0)
 #pragma unroll 1
@@ -431,7 +434,7 @@ __device__ __forceinline__ void merge_unit(const PagedArgs& a, const Merge& u, u
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const int r = warp + 16 * k;
+    const int r = warp + kWarps * k;
     if (r >= rows) break;
     const float inv = L[k] == 0.0f ? 0.0f : 1.0f / L[k];
     const size_t out = (static_cast<size_t>(u.b) * a.Hkv + hk) * a.rows + row0 + r;
@@ -443,7 +446,7 @@ __device__ __forceinline__ void merge_unit(const PagedArgs& a, const Merge& u, u
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kPgThreads, 1)
+__global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const PagedArgs a) {
   using S = PgShape<D, R>;
@@ -471,22 +474,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   } else if (warp == 3) {
     if (lane < 2) {
       mbar_init(&b->q_full[lane], 1);
-      mbar_init(&b->q_empty[lane], 9);
+      mbar_init(&b->q_empty[lane], 1 + 4 * S::kGroups);
       mbar_init(&b->s_full[lane], 1);
-      mbar_init(&b->s_free[lane], 8);
-      mbar_init(&b->p_full[lane], 8);
+      mbar_init(&b->s_free[lane], 4 * S::kGroups);
+      mbar_init(&b->p_full[lane], 4 * S::kGroups);
       mbar_init(&b->pv_done[lane], 1);
       mbar_init(&b->o_full[lane], 1);
       mbar_init(&b->o_free[lane], 4);
-      mbar_init(&b->stats_full[lane], 8);
+      mbar_init(&b->stats_full[lane], 4 * S::kGroups);
     }
     if (lane == 0) {
       mbar_init(&b->merged, 1);
       b->abort = 0u;
     }
     fence_mbar_init();
-  } else if (warp >= 12) {
-    for (int i = threadIdx.x - 384; i < 256; i += 128) b->nan_keys[i >> 7][i & 127] = 0u;
+  } else if (warp >= S::kEpi) {
+    for (int i = threadIdx.x - 32 * S::kEpi; i < 256; i += 128) b->nan_keys[i >> 7][i & 127] = 0u;
   }
   if (R == 8 && warp >= 4 && warp < 8) {             // the zero rows of P^T
     for (int i = threadIdx.x - 128; i < 2 * U * 64; i += 128)
@@ -706,13 +709,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->q_full[qb]);
     }
-  } else if (warp < 12) {
+  } else if (warp < S::kEpi) {
     // ------------------------------------------------------------- softmax
-    // Two groups of four warps; each has half of the rows, for every key.
-    constexpr int H = R / 2;
+    // Groups of four warps; each has its share of the rows, for every key.
+    constexpr int H = S::kRows;
     const int wq = warp & 3;
-    const int half = (warp >> 2) - 1;
-    const int hr = half * H;                         // this group's first row
+    const int group = (warp >> 2) - 1;
+    const int hr = group * H;                        // this group's first row
     const uint32_t lane_base = tmem + (uint32_t(wq * 32) << 16);
     const int page_shift = 31 - __clz(a.page);
     Walk<TILE> walk(a, start, n_tiles);
@@ -766,10 +769,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             s[u][r + 2] = there ? fmaf(s[u][r + 2], qf.z * f.x, f.y) : -INFINITY;
             s[u][r + 3] = there ? fmaf(s[u][r + 3], qf.w * f.x, f.y) : -INFINITY;
           }
-          if (!there) {      // stale codes of V must not meet p = 0; each group clears half of the row
-            uint8_t* v = sKV + st * S::kStageBytes + S::kTileBytes + kt * D + half * (D / 2);
+          if (!there) {      // stale codes of V must not meet p = 0; each group clears its part of the row
+            uint8_t* v = sKV + st * S::kStageBytes + S::kTileBytes + kt * D + group * (D / S::kGroups);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < D / S::kGroups / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         if (a.causal && tile0 + TILE > pc.len - a.Nq + 1) {
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             const int kt = 128 * u + wq * 32 + lane;
             const int edge = tile0 + kt - (pc.len - a.Nq + 1);
             if (edge >= 0 && tile0 + kt < pc.len)
-              ok = clear_nan_codes<D>(sKV + st * S::kStageBytes + S::kTileBytes, kt, half, edge, b->nan_keys[ob],
+              ok = clear_nan_codes<D, S::kGroups>(sKV + st * S::kStageBytes + S::kTileBytes, kt, group, edge, b->nan_keys[ob],
                                       &b->o_free[ob], it, ok, wc);
           }
           ok = __all_sync(0xffffffffu, ok);
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         for (int r = 0; r < H; ++r)
 #pragma unroll
           for (int u = 0; u < U; ++u) need |= s[u][r] > m_used[r] + kRescaleThreshold;
-        if (group_any(1 + half, need)) {
+        if (group_any(1 + group, need)) {
 #pragma unroll
           for (int r = 0; r < H; ++r) {
             float x = s[0][r];
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             x = redux_max(x);
             if (lane == 0) b->red_max[wq][hr + r] = x;
           }
-          group_sync(1 + half);
+          group_sync(1 + group);
           float alpha[H];
 #pragma unroll
           for (int r = 0; r < H; ++r) {
@@ -986,15 +989,15 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         // the unit's CTAs: each has per tiles, so the first began ceil(j0 / per) shares before
         const int c0 = static_cast<int>(blockIdx.x) - (pc.j0 + per - 1) / per;
         const int c1 = static_cast<int>(blockIdx.x) + (pc.nt - pc.j0 - pc.n + per - 1) / per;
-        group_sync(3);
-        if (ok && warp == 12 && mark_done(a.marks, a.nonce, slot, c0, c1, lane) && lane == 0)
+        group_sync(1 + S::kGroups);
+        if (ok && warp == S::kEpi && mark_done(a.marks, a.nonce, slot, c0, c1, lane) && lane == 0)
           b->merge[b->n_merge++] = Merge{pc.b, pc.unit, c0, c1};
       }
     }
   }
   // requests without a token
-  if (warp >= 12) {
-    const int t = threadIdx.x - 384;
+  if (warp >= S::kEpi) {
+    const int t = threadIdx.x - 32 * S::kEpi;
     for (int i = blockIdx.x; i < a.B; i += kPagedCtas) {
       if (pg_len(a, i) > 0) continue;
       const size_t rows = static_cast<size_t>(a.Hkv) * a.rows;
@@ -1029,7 +1032,7 @@ cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const P
     if (e != cudaSuccess) return e;
     if (dev <= 63) configured.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch_dependent(kern, dim3(kPagedCtas), dim3(kPgThreads), smem, stream, tk, tv, a);
+  return launch_dependent(kern, dim3(kPagedCtas), dim3(PgShape<D, R>::kThreads), smem, stream, tk, tv, a);
 }
 
 }  // namespace
