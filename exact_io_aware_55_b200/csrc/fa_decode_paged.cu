@@ -38,8 +38,8 @@
 // unit combines them by their log-sum-exp, in the order of the pieces, so that
 // results do not depend on timing.
 //
-// Warps: 0 page ids and TMA, 1 MMA issuer and TMEM owner, 2 page scales,
-// 3 queries, from 4 on the softmax groups of four (thread = key, each group its
+// Warps: 0 page ids and TMA, 1 S products and TMEM owner, 2 page scales and
+// queries, 3 PV products, from 4 on the softmax groups of four (thread = key, each group its
 // share of the rows; TMEM lane quarter = warp % 4), the last four epilogue.  Pages that lie behind the length or outside the cache are not
 // loaded; the softmax warps clear the V rows of keys that are not there, since
 // p = 0 times a stale NaN code would be NaN.
@@ -62,15 +62,20 @@ constexpr float kBase = 1024.0f;            // P is scaled by 2^10: below 2^15, 
 
 template <int D, int R>
 struct PgShape {
-  static constexpr int kGroups = R == 32 ? 4 : 2;             // of softmax warps
-  static constexpr int kRows = R / kGroups;                   // rows of each
+  // Groups of softmax warps: kSplit share a tile's rows, kTurns take the tiles
+  // in turn, each with a maximum, a sum and an O of its own.
+  static constexpr int kSplit = R / 8;
+  static constexpr int kTurns = R == 32 ? 1 : 2;
+  static constexpr int kGroups = kSplit * kTurns;
+  static constexpr int kRows = R / kSplit;                    // rows of a group
   static constexpr int kEpi = 4 + 4 * kGroups;                // first epilogue warp
   static constexpr int kThreads = 32 * (kEpi + 4);
   static constexpr int kSub = (D == 64) ? 2 : 1;              // 128-key sub-tiles per tile
   static constexpr int kTileKeys = 128 * kSub;
   static constexpr int kTileBytes = kTileKeys * D;            // K (or V) codes of one tile
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kNS = (R == 32) ? 5 : 6;               // ring depth: 160 or 192 KB
+  static constexpr int kBufs = 2 * kTurns;                    // of S^T and of the queries
+  static constexpr int kNS = (R == 32 || (D == 64 && R == 16)) ? 5 : 6;   // ring depth: 160 or 192 KB
   static constexpr int kMaxPages = kTileKeys / 16;
   static constexpr int kQRows = 2 * R;                        // hi, lo
   static constexpr int kQBytes = kQRows * D;
@@ -81,9 +86,9 @@ struct PgShape {
   static constexpr int kPvSteps = kTileKeys / 32;             // O^T k-steps per tile
   static constexpr uint32_t kIdS = idesc_e4m3(128, kQRows, false, false);
   static constexpr uint32_t kIdO = idesc_e4m3(D, kPRows, true, false) | (1u << 10);   // B format 1: e5m2
-  static constexpr uint32_t kColS = 0;                        // two S^T buffers of kQRows * kSub columns
-  static constexpr uint32_t kColO = 2 * kQRows * kSub;        // two O^T buffers of kPRows columns
-  static constexpr uint32_t kCols = kColO + 2 * kPRows;
+  static constexpr uint32_t kColS = 0;                        // kBufs S^T buffers of kQRows * kSub columns
+  static constexpr uint32_t kColO = kBufs * kQRows * kSub;        // two O^T buffers of kPRows columns per turn
+  static constexpr uint32_t kCols = kColO + 2 * kTurns * kPRows;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "TMEM columns");
 };
@@ -97,20 +102,20 @@ struct Place {
   int b, unit, j, len, nt;
 };
 
-template <int R, int NS, int PAGES>
+template <int R, int NS, int PAGES, int TURNS, int BUFS>
 struct PgBarriers {
   uint64_t kv_full[NS], kv_empty[NS];
-  uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], s_free[2];
-  uint64_t p_full[2], pv_done[2];
+  uint64_t q_full[BUFS], q_empty[BUFS];
+  uint64_t s_full[BUFS], s_free[BUFS];
+  uint64_t p_full[2];
   uint64_t o_full[2], o_free[2];
   uint64_t stats_full[2];
   uint64_t merged;
   alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, e, 2^-e, vs / 2^e
-  alignas(16) float q_factor[2][R];        // power of two that a row of queries was divided by
-  alignas(16) float red_max[4][R];         // per-warp tile maxima (log2 units)
-  alignas(16) float stat_m[2][R];          // piece's running max
-  alignas(16) float stat_l[2][4][R];       // piece's per-warp sums
+  alignas(16) float q_factor[BUFS][R];        // power of two that a row of queries was divided by
+  alignas(16) float red_max[TURNS][4][R];  // per-warp tile maxima (log2 units)
+  alignas(16) float stat_m[2][TURNS][R];     // piece's running max
+  alignas(16) float stat_l[2][TURNS][4][R];  // piece's per-warp sums
   uint32_t nan_keys[2][128];               // per column of a piece: boundary keys whose V code is NaN
   int per, n_tiles;
   int n_merge;                             // units that this CTA is the last to have finished a piece of
@@ -121,12 +126,12 @@ struct PgBarriers {
 };
 
 template <int D, int R>
-using PgBar = PgBarriers<R, PgShape<D, R>::kNS, PgShape<D, R>::kMaxPages>;
+using PgBar = PgBarriers<R, PgShape<D, R>::kNS, PgShape<D, R>::kMaxPages, PgShape<D, R>::kTurns, PgShape<D, R>::kBufs>;
 
 template <int D, int R>
 constexpr size_t pg_smem_bytes() {
   using S = PgShape<D, R>;
-  return 1024 + size_t(S::kNS) * S::kStageBytes + 2 * S::kQBytes + 2 * S::kPBytes + sizeof(PgBar<D, R>);
+  return 1024 + size_t(S::kNS) * S::kStageBytes + S::kBufs * S::kQBytes + 2 * S::kPBytes + sizeof(PgBar<D, R>);
 }
 
 // Shared-memory matrix descriptor: rows of D bytes, swizzled over D bytes.
@@ -171,7 +176,11 @@ __device__ __noinline__ bool pg_wait_slow(uint64_t* bar, uint32_t parity, const 
 __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t where) {
   return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || pg_wait_slow(bar, parity, w, where);
 }
-// Three waits whose first looks overlap.
+// Two and three waits whose first looks overlap.
+__device__ __forceinline__ bool pg_wait2(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, const WaitCtx& w, uint32_t where) {
+  const bool a = mbar_try_wait(x, px), b = mbar_try_wait(y, py);
+  return __all_sync(0xffffffffu, a && b) || (pg_wait_slow(x, px, w, where) && pg_wait_slow(y, py, w, where));
+}
 __device__ __forceinline__ bool pg_wait3(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, uint64_t* z, uint32_t pz,
                                          const WaitCtx& w, uint32_t where) {
   const bool a = mbar_try_wait(x, px), b = mbar_try_wait(y, py), c = mbar_try_wait(z, pz);
@@ -223,11 +232,30 @@ __device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[N]) {
   else
     tmem_st_x16(t, r);
 }
-__device__ __forceinline__ float warp_sum(float x) {
+// Sums over the warp of H = 8 values per lane; lane gets that of value
+// lane / 4.  Each step but the last two halves the values: a lane keeps one half
+// and hands the other to its partner.
+template <int H>
+__device__ __forceinline__ float rows_sum(const float (&x)[H], int lane) {
+  static_assert(H == 8, "three halvings");
+  float y[4], z[2];
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  return x;
+  for (int k = 0; k < 4; ++k) {
+    const float keep = lane & 16 ? x[4 + k] : x[k], give = lane & 16 ? x[k] : x[4 + k];
+    y[k] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float keep = lane & 8 ? y[2 + k] : y[k], give = lane & 8 ? y[k] : y[2 + k];
+    z[k] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+  }
+  const float keep = lane & 4 ? z[1] : z[0], give = lane & 4 ? z[0] : z[1];
+  float w = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+  w += __shfl_xor_sync(0xffffffffu, w, 2);
+  return w + __shfl_xor_sync(0xffffffffu, w, 1);
 }
+
+__device__ __forceinline__ int kv_head(const PagedArgs& a, int unit) { return a.row_tiles == 1 ? unit : unit / a.row_tiles; }
 
 // Two bf16 queries times `inv` (below 256) as two e4m3 parts each: the value
 // rounded, and 16 times what is left of it.
@@ -263,12 +291,61 @@ __device__ __noinline__ bool clear_nan_codes(uint8_t* v, int kt, int part, int e
   return ok;
 }
 
-__device__ __forceinline__ int kv_head(const PagedArgs& a, int unit) { return a.row_tiles == 1 ? unit : unit / a.row_tiles; }
-
 // A piece: tiles [j0, j0 + n) of one unit.
 struct Piece {
   int b, unit, len, nt, j0, n;
 };
+// Query rows become two e4m3 parts each, by one warp, eight rows at a time, four
+// lanes to a row.  Loading and splitting are apart, so that the next piece's
+// rows come in while this one's work goes on.
+template <int D>
+struct QueryRows {
+  static constexpr int kChunks = D / 32;             // 16-byte groups of eight elements per lane
+  uint4 w[kChunks];
+  // rows first..first + 7 of (b, unit), zeros behind the last row
+  template <int R>
+  __device__ __forceinline__ void load(const PagedArgs& a, const Piece& pc, int first, int lane) {
+    const int hk = kv_head(a, pc.unit);
+    const int row = (pc.unit - hk * a.row_tiles) * R + first + (lane >> 2);
+    const uint4* q = static_cast<const uint4*>(a.q) +
+                     ((static_cast<size_t>(pc.b) * a.Hkv + hk) * a.rows + row) * (D / 8) + (lane & 3) * kChunks;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) w[c] = row < a.rows ? q[c] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  // as rows first.. (hi) and R + first.. (lo) of the B operand, and the powers
+  // of two that the rows were divided by
+  template <int R>
+  __device__ __forceinline__ void split(uint8_t* dst, float* factor, int first, int lane) const {
+    const int r = first + (lane >> 2);
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const uint32_t x = __vmaxu2(__vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu),
+                                  __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu));
+      top = max(top, max(x & 0xffffu, x >> 16));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // the row times 2^-e has its largest element in [128, 256)
+    const int e = min(max(static_cast<int>(top >> 7) - 134, -110), 121);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) split_pair(x[k], inv, hi[k], lo[k]);
+      const int place = (lane & 3) * (D / 64) + (c >> 1);
+      *reinterpret_cast<uint2*>(dst + pg_unit<D>(r, place) + (c & 1) * 8) =
+          make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+      *reinterpret_cast<uint2*>(dst + pg_unit<D>(R + r, place) + (c & 1) * 8) =
+          make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+    }
+    // a row that holds something not finite has no scores
+    if ((lane & 3) == 0) factor[r] = top >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  }
+};
+
 // Walks over a CTA's range of tiles; `left` are to come.
 template <int TILE>
 struct Walk {
@@ -455,8 +532,8 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;                               // NS x (K tile, V tile)
   uint8_t* sP = sKV + NS * S::kStageBytes;           // 2 x P^T
-  uint8_t* sQ = sP + 2 * S::kPBytes;                 // 2 x (hi, lo) queries
-  auto* b = reinterpret_cast<PgBar<D, R>*>(sQ + 2 * S::kQBytes);
+  uint8_t* sQ = sP + 2 * S::kPBytes;                 // kBufs x (hi, lo) queries
+  auto* b = reinterpret_cast<PgBar<D, R>*>(sQ + S::kBufs * S::kQBytes);
   const WaitCtx wc{&b->abort, a.status, FA_WAIT_LIMIT_NS};
 
   const int warp = threadIdx.x >> 5;
@@ -472,13 +549,14 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     }
     fence_mbar_init();
   } else if (warp == 3) {
-    if (lane < 2) {
+    if (lane < S::kBufs) {
       mbar_init(&b->q_full[lane], 1);
       mbar_init(&b->q_empty[lane], 1 + 4 * S::kGroups);
       mbar_init(&b->s_full[lane], 1);
-      mbar_init(&b->s_free[lane], 4 * S::kGroups);
-      mbar_init(&b->p_full[lane], 4 * S::kGroups);
-      mbar_init(&b->pv_done[lane], 1);
+      mbar_init(&b->s_free[lane], 4 * S::kSplit);
+    }
+    if (lane < 2) {
+      mbar_init(&b->p_full[lane], 4 * S::kSplit);
       mbar_init(&b->o_full[lane], 1);
       mbar_init(&b->o_free[lane], 4);
       mbar_init(&b->stats_full[lane], 4 * S::kGroups);
@@ -575,65 +653,80 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       row = next;
     }
   } else if (warp == 1) {
-    // ----------------------------------------------------------------- MMA
+    // ------------------------------------------------------------------- S
     const uint64_t dK = pg_desc<D>(smem_u32(sKV));                              // K tiles, K-major (A)
-    const uint64_t dV = pg_desc<D>(smem_u32(sKV + S::kTileBytes));              // V tiles, MN-major (A of O^T)
     const uint64_t dQ = pg_desc<D>(smem_u32(sQ));                               // queries, K-major (B)
+    Walk<TILE> walk(a, start, n_tiles);
+    Piece pc;
+    int left = 0;                                    // tiles of the piece
+    for (int g = 0, it = -1; g < n_tiles; ++g) {
+      const bool begins = left == 0;
+      if (begins) {
+        walk.next(pc);
+        left = pc.n;
+        ++it;
+      }
+      const int s = g % NS, sb = g % S::kBufs, qb = it % S::kBufs;
+      uint64_t* q_bar = &b->q_full[qb];
+      // before its first use an S buffer is free: look at the K barrier twice
+      const bool used = g >= S::kBufs;
+      if ((begins && !pg_wait(q_bar, (it / S::kBufs) & 1, wc, WAIT_PAGED_Q)) ||
+          !pg_wait2(&b->kv_full[s], (g / NS) & 1, used ? &b->s_free[sb] : &b->kv_full[s],
+                    (used ? (g / S::kBufs) + 1 : g / NS) & 1, wc, WAIT_PAGED_KV))
+        break;
+      tc_fence_after();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int ks = 0; ks < S::kKSteps; ++ks) {
+          const uint64_t ka = uint64_t((s * S::kStageBytes + u * 128 * D + ks * 32) >> 4);
+          const uint64_t qo = uint64_t((qb * S::kQBytes + ks * 32) >> 4);
+          mma_f8_ss_e(tmem + S::kColS + S::kQRows * (sb * U + u), dK + ka, dQ + qo, S::kIdS, ks > 0 ? 1u : 0u);
+        }
+      tc_commit_e(&b->s_full[sb]);
+      if (--left == 0) tc_commit_e(&b->q_empty[qb]);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ PV
+    const uint64_t dV = pg_desc<D>(smem_u32(sKV + S::kTileBytes));              // V tiles, MN-major (A)
     const uint64_t dP = sdesc_sw128(smem_u32(sP), 16, 1024);                    // P^T, K-major (B)
     Walk<TILE> walk(a, start, n_tiles);
     Piece pc;
-    // Turn g issues S of tile g and PV of tile g - 1, which may belong to the
-    // piece before.
-    int it = -1, j = 0, n = 0;                       // tile g: piece, tile of the piece, its tiles
-    for (int g = 0; g <= n_tiles; ++g) {
-      const int prev_it = it;
-      const bool prev_first = j == 1, prev_last = j == n;      // of tile g - 1
-      if (g < n_tiles) {
-        if (j == n) {
-          walk.next(pc);
-          n = pc.n;
-          j = 0;
-          ++it;
-        }
-        const int s = g % NS, sb = g & 1, qb = it & 1;
-        if ((j == 0 && !pg_wait(&b->q_full[qb], (it >> 1) & 1, wc, WAIT_PAGED_Q)) ||
-            !pg_wait(&b->kv_full[s], (g / NS) & 1, wc, WAIT_PAGED_KV) ||
-            (g >= 2 && !pg_wait(&b->s_free[sb], ((g >> 1) + 1) & 1, wc, WAIT_PAGED_S_FREE)))
-          break;
-        tc_fence_after();
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int ks = 0; ks < S::kKSteps; ++ks) {
-            const uint64_t ka = uint64_t((s * S::kStageBytes + u * 128 * D + ks * 32) >> 4);
-            const uint64_t qo = uint64_t((qb * S::kQBytes + ks * 32) >> 4);
-            mma_f8_ss_e(tmem + S::kColS + S::kQRows * (sb * U + u), dK + ka, dQ + qo, S::kIdS, ks > 0 ? 1u : 0u);
-          }
-        tc_commit_e(&b->s_full[sb]);
-        if (++j == n) tc_commit_e(&b->q_empty[qb]);
+    int j = 0, n = 0;                                // tile of the piece, its tiles
+    for (int g = 0, it = -1; g < n_tiles; ++g, ++j) {
+      if (j == n) {
+        walk.next(pc);
+        n = pc.n;
+        j = 0;
+        ++it;
       }
-      if (g > 0) {
-        const int s = (g - 1) % NS, pb = (g - 1) & 1, ob = prev_it & 1;
-        if ((prev_first && prev_it >= 2 && !pg_wait(&b->o_free[ob], ((prev_it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE)) ||
-            !pg_wait(&b->p_full[pb], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_P))
-          break;
-        tc_fence_after();
+      const int s = g % NS, pb = g & 1, ob = it & 1;
+      const bool first = j < S::kTurns;              // into its turn's O
+      const uint32_t col_o = tmem + S::kColO + S::kPRows * (S::kTurns * ob + g % S::kTurns);
+      if ((j == 0 && it >= 2 && !pg_wait(&b->o_free[ob], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE)) ||
+          !pg_wait(&b->p_full[pb], (g >> 1) & 1, wc, WAIT_PAGED_P))
+        break;
+      tc_fence_after();
 #pragma unroll
-        for (int kt = 0; kt < S::kPvSteps; ++kt) {
-          const uint64_t va = uint64_t((s * S::kStageBytes + kt * 32 * D) >> 4);
-          const uint64_t po = uint64_t((pb * S::kPBytes + (kt >> 2) * S::kPSub + (kt & 3) * 32) >> 4);
-          mma_f8_ss_e(tmem + S::kColO + S::kPRows * ob, dV + va, dP + po, S::kIdO, (!prev_first || kt > 0) ? 1u : 0u);
-        }
-        tc_commit_e(&b->pv_done[pb]);
-        tc_commit_e(&b->kv_empty[s]);
-        if (prev_last) tc_commit_e(&b->o_full[ob]);
+      for (int kt = 0; kt < S::kPvSteps; ++kt) {
+        const uint64_t va = uint64_t((s * S::kStageBytes + kt * 32 * D) >> 4);
+        const uint64_t po = uint64_t((pb * S::kPBytes + (kt >> 2) * S::kPSub + (kt & 3) * 32) >> 4);
+        mma_f8_ss_e(col_o, dV + va, dP + po, S::kIdO, (!first || kt > 0) ? 1u : 0u);
       }
+      tc_commit_e(&b->kv_empty[s]);                  // P is read with V, and O has the tile
+      if (j + 1 == n) tc_commit_e(&b->o_full[ob]);
     }
   } else if (warp == 2) {
-    // --------------------------------------------------------- page scales
+    // --------------------------------------------- page scales and queries
     PageBatch<TILE> pb(a, start, n_tiles, lane);
     int row = pb.fetch();
     float ks = row >= 0 ? a.k_scale[row] : 0.0f, vs = row >= 0 ? a.v_scale[row] : 0.0f;
+    Walk<TILE> walk(a, start, n_tiles);
+    Piece pc, coming;
+    walk.next(coming);
+    QueryRows<D> rows;
+    rows.template load<R>(a, coming, 0, lane);
+    int it = 0, left = 0;                            // pieces begun, tiles left of the last
     bool ok = true;
     for (int t0 = 0; t0 < n_tiles && ok; t0 += pb.tiles) {
       const int next = pb.fetch();
@@ -644,6 +737,29 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       const float4 f = row >= 0 ? make_float4(ks * a.c_log2, static_cast<float>(e), inv, vs * inv * kBase)
                                 : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
       for (int u = 0; u < m; ++u) {
+        if (left == 0) {
+          pc = coming;
+          left = pc.n;
+          const int qb = it % S::kBufs;
+          if (it >= S::kBufs && !pg_wait(&b->q_empty[qb], ((it / S::kBufs) + 1) & 1, wc, WAIT_PAGED_Q_EMPTY)) {
+            ok = false;
+            break;
+          }
+#pragma unroll 1
+          for (int first = 0;;) {
+            rows.template split<R>(sQ + qb * S::kQBytes, b->q_factor[qb], first, lane);
+            first += 8;
+            if (first == R) break;
+            rows.template load<R>(a, pc, first, lane);
+          }
+          const bool more = walk.next(coming);
+          if (more) rows.template load<R>(a, coming, 0, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b->q_full[qb]);
+          ++it;
+        }
+        --left;
         const int t = t0 + u, s = t % NS;
         if (t >= NS && !pg_wait(&b->kv_empty[s], ((t / NS) + 1) & 1, wc, WAIT_PAGED_SC_EMPTY)) {
           ok = false;
@@ -657,65 +773,14 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       ks = row >= 0 ? a.k_scale[row] : 0.0f;
       vs = row >= 0 ? a.v_scale[row] : 0.0f;
     }
-  } else if (warp == 3) {
-    // ------------------------------------------------------------- queries
-    // Eight rows at a time, four lanes to a row; the code of all roles together
-    // should stay in the instruction cache, so its loops are not unrolled.
-    constexpr int kChunks = D / 32;                  // 16-byte groups of eight elements per lane
-    Walk<TILE> walk(a, start, n_tiles);
-    Piece pc;
-    for (int it = 0; walk.next(pc); ++it) {
-      const int qb = it & 1;
-      if (it >= 2 && !pg_wait(&b->q_empty[qb], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_Q_EMPTY)) break;
-      const int hk = kv_head(a, pc.unit);
-      const int r0 = (pc.unit - hk * a.row_tiles) * R;
-      const uint4* q = static_cast<const uint4*>(a.q) +
-                       ((static_cast<size_t>(pc.b) * a.Hkv + hk) * a.rows + r0) * (D / 8) + (lane & 3) * kChunks;
-      uint8_t* dst = sQ + qb * S::kQBytes;
-#pragma unroll 1
-      for (int r = lane >> 2; r < R; r += 8) {
-        uint4 w[kChunks];
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) w[c] = r0 + r < a.rows ? q[static_cast<size_t>(r) * (D / 8) + c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const uint32_t x = __vmaxu2(__vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu),
-                                      __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu));
-          top = max(top, max(x & 0xffffu, x >> 16));
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the row times 2^-e has its largest element in [128, 256)
-        const int e = min(max(static_cast<int>(top >> 7) - 134, -110), 121);
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) split_pair(x[k], inv, hi[k], lo[k]);
-          const int unit = (lane & 3) * (D / 64) + (c >> 1);
-          *reinterpret_cast<uint2*>(dst + pg_unit<D>(r, unit) + (c & 1) * 8) =
-              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(dst + pg_unit<D>(R + r, unit) + (c & 1) * 8) =
-              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-        }
-        // a row that holds something not finite has no scores
-        if ((lane & 3) == 0)
-          b->q_factor[qb][r] = top >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->q_full[qb]);
-    }
   } else if (warp < S::kEpi) {
     // ------------------------------------------------------------- softmax
-    // Groups of four warps; each has its share of the rows, for every key.
+    // Groups of four warps; each has its share of the rows, and its turns of the tiles.
     constexpr int H = S::kRows;
     const int wq = warp & 3;
     const int group = (warp >> 2) - 1;
-    const int hr = group * H;                        // this group's first row
+    const int part = group % S::kSplit, turn = group / S::kSplit;
+    const int hr = part * H;                        // this group's first row
     const uint32_t lane_base = tmem + (uint32_t(wq * 32) << 16);
     const int page_shift = 31 - __clz(a.page);
     Walk<TILE> walk(a, start, n_tiles);
@@ -725,7 +790,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     bool ok = true;
     int g = 0, it = 0;
     for (; walk.next(pc); ++it) {
-      const int ob = it & 1, qb = it & 1;
+      const int ob = it & 1, qb = it % S::kBufs;
       const int row0 = (a.row_tiles == 1 ? 0 : pc.unit % a.row_tiles) * R + hr;
       float m_used[H], l_t[H];
 #pragma unroll
@@ -733,11 +798,13 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         m_used[r] = -INFINITY;
         l_t[r] = 0.0f;
       }
+      bool began = false;                            // O holds a tile of this piece
       for (int j = 0; j < pc.n; ++j, ++g) {
-        const int sb = g & 1, st = g % NS;
+        if (g % S::kTurns != turn) continue;
+        const int sb = g % S::kBufs, st = g % NS;
         // with S come the page factors (kv_full) and the queries' factors (q_full)
-        ok = ok && pg_wait3(&b->kv_full[st], (g / NS) & 1, &b->q_full[qb], (it >> 1) & 1, &b->s_full[sb],
-                                   (g >> 1) & 1, wc, WAIT_PAGED_S);
+        ok = ok && pg_wait3(&b->kv_full[st], (g / NS) & 1, &b->q_full[qb], (it / S::kBufs) & 1, &b->s_full[sb],
+                            (g / S::kBufs) & 1, wc, WAIT_PAGED_S);
         tc_fence_after();
         const int tile0 = (pc.j0 + j) * TILE;
         float s[U][H];
@@ -770,9 +837,9 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             s[u][r + 3] = there ? fmaf(s[u][r + 3], qf.w * f.x, f.y) : -INFINITY;
           }
           if (!there) {      // stale codes of V must not meet p = 0; each group clears its part of the row
-            uint8_t* v = sKV + st * S::kStageBytes + S::kTileBytes + kt * D + group * (D / S::kGroups);
+            uint8_t* v = sKV + st * S::kStageBytes + S::kTileBytes + kt * D + part * (D / S::kSplit);
 #pragma unroll
-            for (int c = 0; c < D / S::kGroups / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < D / S::kSplit / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         if (a.causal && tile0 + TILE > pc.len - a.Nq + 1) {
@@ -783,7 +850,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             const int kt = 128 * u + wq * 32 + lane;
             const int edge = tile0 + kt - (pc.len - a.Nq + 1);
             if (edge >= 0 && tile0 + kt < pc.len)
-              ok = clear_nan_codes<D, S::kGroups>(sKV + st * S::kStageBytes + S::kTileBytes, kt, group, edge, b->nan_keys[ob],
+              ok = clear_nan_codes<D, S::kSplit>(sKV + st * S::kStageBytes + S::kTileBytes, kt, part, edge, b->nan_keys[ob],
                                       &b->o_free[ob], it, ok, wc);
           }
           ok = __all_sync(0xffffffffu, ok);
@@ -805,31 +872,46 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           for (int u = 0; u < U; ++u) need |= s[u][r] > m_used[r] + kRescaleThreshold;
         if (group_any(1 + group, need)) {
 #pragma unroll
-          for (int r = 0; r < H; ++r) {
-            float x = s[0][r];
+          for (int r = 0; r < H; r += 4) {
+            float x[4];
 #pragma unroll
-            for (int u = 1; u < U; ++u) x = fmaxf(x, s[u][r]);
-            x = redux_max(x);
-            if (lane == 0) b->red_max[wq][hr + r] = x;
+            for (int k = 0; k < 4; ++k) {
+              x[k] = s[0][r + k];
+#pragma unroll
+              for (int u = 1; u < U; ++u) x[k] = fmaxf(x[k], s[u][r + k]);
+              x[k] = redux_max(x[k]);
+            }
+            if (lane == 0) *reinterpret_cast<float4*>(&b->red_max[turn][wq][hr + r]) = make_float4(x[0], x[1], x[2], x[3]);
           }
           group_sync(1 + group);
-          float alpha[H];
+          float before[H];
 #pragma unroll
-          for (int r = 0; r < H; ++r) {
-            const float mt = fmaxf(fmaxf(b->red_max[0][hr + r], b->red_max[1][hr + r]),
-                                   fmaxf(b->red_max[2][hr + r], b->red_max[3][hr + r]));
-            const float mn = fmaxf(m_used[r], mt);
-            alpha[r] = (mn == -INFINITY) ? 1.0f : ex2_approx(m_used[r] - mn);
-            m_used[r] = mn;
-            l_t[r] *= alpha[r];
+          for (int r = 0; r < H; r += 4) {
+            const float4 x0 = *reinterpret_cast<const float4*>(&b->red_max[turn][0][hr + r]);
+            const float4 x1 = *reinterpret_cast<const float4*>(&b->red_max[turn][1][hr + r]);
+            const float4 x2 = *reinterpret_cast<const float4*>(&b->red_max[turn][2][hr + r]);
+            const float4 x3 = *reinterpret_cast<const float4*>(&b->red_max[turn][3][hr + r]);
+            const float x[4] = {fmaxf(fmaxf(x0.x, x1.x), fmaxf(x2.x, x3.x)), fmaxf(fmaxf(x0.y, x1.y), fmaxf(x2.y, x3.y)),
+                                fmaxf(fmaxf(x0.z, x1.z), fmaxf(x2.z, x3.z)), fmaxf(fmaxf(x0.w, x1.w), fmaxf(x2.w, x3.w))};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              before[r + k] = m_used[r + k];
+              m_used[r + k] = fmaxf(m_used[r + k], x[k]);
+            }
           }
-          if (j > 0) {   // O^T holds earlier tiles of this piece: rescale it once PV(g-1) is done
-            ok = ok && pg_wait(&b->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wc, WAIT_PAGED_PV);
+          if (began) {   // rescale O^T, once the last product into it is done
+            ok = ok && pg_wait(&b->kv_empty[(g - S::kTurns) % NS], ((g - S::kTurns) / NS) & 1, wc, WAIT_PAGED_PV);
             tc_fence_after();
+            float alpha[H];
+#pragma unroll
+            for (int r = 0; r < H; ++r) {
+              alpha[r] = m_used[r] == -INFINITY ? 1.0f : ex2_approx(before[r] - m_used[r]);
+              l_t[r] *= alpha[r];
+            }
             if (ok) {
 #pragma unroll
-              for (int part = 0; part < 3; ++part) {
-                const uint32_t col = lane_base + S::kColO + S::kPRows * ob + part * R + hr;
+              for (int k = 0; k < 3; ++k) {
+                const uint32_t col = lane_base + S::kColO + S::kPRows * (S::kTurns * ob + turn) + k * R + hr;
                 uint32_t o[H];
                 tmem_ld<H>(col, o);
 #pragma unroll
@@ -842,8 +924,10 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         }
         // P^T into shared memory: B operand, K-major, rows = parts of the query
         // rows, the sub-tile's 128 keys in one 128-byte swizzled row.  The
-        // buffer is free: S(g) was committed behind PV(g - 2), which read it.
+        // buffer is free once PV(g - 2) has read it, which gave its stage back.
+        began = true;
         const int pb = g & 1;
+        if (g >= 2) ok = ok && pg_wait(&b->kv_empty[(g - 2) % NS], ((g - 2) / NS) & 1, wc, WAIT_PAGED_PV);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int key = wq * 32 + lane;
@@ -863,10 +947,9 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             const uint32_t mid = (*reinterpret_cast<const uint32_t*>(&d1) + 0x00800080u) & 0xff00ff00u;
             const __half2 d2 = __hmul2(__hsub2(d1, *reinterpret_cast<const __half2*>(&mid)), __float2half2_rn(8.0f));
             const uint32_t lo = *reinterpret_cast<const uint32_t*>(&d2) + 0x00800080u;
-            // hr is 4 or a multiple of 8: row & 7 as the swizzle sees it
-            const int x0 = ((H == 4 ? hr : 0) + r) & 7;
-            uint8_t* p_even = pbase + r * 128 + ((unit ^ x0) << 4);
-            uint8_t* p_odd = pbase + (r + 1) * 128 + ((unit ^ (x0 + 1)) << 4);
+            // hr is a multiple of 8: the swizzle goes by r
+            uint8_t* p_even = pbase + r * 128 + ((unit ^ (r & 7)) << 4);
+            uint8_t* p_odd = pbase + (r + 1) * 128 + ((unit ^ ((r + 1) & 7)) << 4);
             p_even[0] = static_cast<uint8_t>(hi >> 8);
             p_odd[0] = static_cast<uint8_t>(hi >> 24);
             p_even[R * 128] = static_cast<uint8_t>(mid >> 8);
@@ -880,17 +963,22 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&b->p_full[pb]);
       }
-      if (ok && lane == 0) mbar_arrive(&b->q_empty[qb]);
       // Piece done: publish the running max and the per-warp sums, once the
-      // epilogue has let go of this buffer two pieces ago.
+      // epilogue has let go of this buffer two pieces ago.  That every group had
+      // left that piece is also why this one, which may have had no tile to wait
+      // for in this piece, is not ahead of q_empty's phase.
       if (it >= 2) ok = ok && pg_wait(&b->o_free[ob], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE);
+      if (ok && lane == 0) mbar_arrive(&b->q_empty[qb]);
+      if (ok && began) {
+        const float l = rows_sum<H>(l_t, lane);      // of row lane / (32 / H)
+        if (lane % (32 / H) == 0) b->stat_l[ob][turn][wq][hr + lane / (32 / H)] = l;
+        if (wq == 0 && lane == 0) {
+          // scores that are all NaN leave no maximum, but a sum to be seen
 #pragma unroll
-      for (int r = 0; r < H; ++r) {
-        const float l = warp_sum(l_t[r]);
-        if (ok && lane == 0) {
-          b->stat_l[ob][wq][hr + r] = l;
-          if (wq == 0) b->stat_m[ob][hr + r] = m_used[r];
+          for (int r = 0; r < H; ++r) b->stat_m[ob][turn][hr + r] = m_used[r] == -INFINITY && l_t[r] != l_t[r] ? 0.0f : m_used[r];
         }
+      } else if (ok && wq == 0 && lane < H) {
+        b->stat_m[ob][turn][hr + lane] = -INFINITY;  // no tile of the piece: the sums are not looked at
       }
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&b->stats_full[ob]);
@@ -914,13 +1002,25 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       const int row0 = (pc.unit - hk * a.row_tiles) * R;
       const int rows = min(R, a.rows - row0);
       const size_t out = (static_cast<size_t>(pc.b) * a.Hkv + hk) * a.rows + row0;
-      // lane r has row r's sum
-      float inv = 0.0f;
+      // lane r has row r's sum, and the factor of each turn's O: a turn without a
+      // visible key has none (its O may never have been written)
+      float f[S::kTurns] = {};
       if (ok && lane < rows) {
-        const float L = b->stat_l[ob][0][lane] + b->stat_l[ob][1][lane] + b->stat_l[ob][2][lane] + b->stat_l[ob][3][lane];
-        inv = L == 0.0f ? 0.0f : (1.0f / kBase) / L;
+        float M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int k = 0; k < S::kTurns; ++k) M = fmaxf(M, b->stat_m[ob][k][lane]);
+#pragma unroll
+        for (int k = 0; k < S::kTurns; ++k) {
+          const float m = b->stat_m[ob][k][lane];
+          f[k] = m == -INFINITY ? 0.0f : ex2_approx(m - M);
+          if (m != -INFINITY)
+            L = fmaf(f[k], b->stat_l[ob][k][0][lane] + b->stat_l[ob][k][1][lane] + b->stat_l[ob][k][2][lane] + b->stat_l[ob][k][3][lane], L);
+        }
+        const float inv = L == 0.0f ? 0.0f : (1.0f / kBase) / L;
+#pragma unroll
+        for (int k = 0; k < S::kTurns; ++k) f[k] *= inv;
         if (wq == 0) {
-          const float lse = L == 0.0f ? -INFINITY : (b->stat_m[ob][lane] + log2f(L)) * kLn2;
+          const float lse = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
           if (whole)
             a.lse[out + lane] = lse;
           else
@@ -934,30 +1034,35 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 #pragma unroll 1
       for (int rg = 0; rg < R; rg += kStep) {
         float o[kStep];
-        if constexpr (R == 8) {
-          uint32_t x[32];
-          tmem_ld_x32(lane_base + S::kColO + S::kPRows * ob, x);
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            o[r] = fmaf(__uint_as_float(x[16 + r]), 1.0f / 64.0f,
-                        fmaf(__uint_as_float(x[8 + r]), 0.125f, __uint_as_float(x[r])));
-        } else {
-          uint32_t x[16];
-          const uint32_t col = lane_base + S::kColO + S::kPRows * ob + rg;
-          tmem_ld_x16(col + 2 * R, x);
+        for (int t = 0; t < S::kTurns; ++t) {
+          float v[kStep];
+          const uint32_t col = lane_base + S::kColO + S::kPRows * (S::kTurns * ob + t) + rg;
+          if constexpr (R == 8) {
+            uint32_t x[32];
+            tmem_ld_x32(col, x);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] = __uint_as_float(x[r]) * (1.0f / 64.0f);
-          tmem_ld_x16(col + R, x);
+            for (int r = 0; r < 8; ++r)
+              v[r] = fmaf(__uint_as_float(x[16 + r]), 1.0f / 64.0f,
+                          fmaf(__uint_as_float(x[8 + r]), 0.125f, __uint_as_float(x[r])));
+          } else {
+            uint32_t x[16];
+            tmem_ld_x16(col + 2 * R, x);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] = fmaf(__uint_as_float(x[r]), 0.125f, o[r]);
-          tmem_ld_x16(col, x);
+            for (int r = 0; r < 16; ++r) v[r] = __uint_as_float(x[r]) * (1.0f / 64.0f);
+            tmem_ld_x16(col + R, x);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] += __uint_as_float(x[r]);
-        }
+            for (int r = 0; r < 16; ++r) v[r] = fmaf(__uint_as_float(x[r]), 0.125f, v[r]);
+            tmem_ld_x16(col, x);
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          const float f = __shfl_sync(0xffffffffu, inv, rg + k);
-          o[k] = f == 0.0f ? 0.0f : o[k] * f;
+            for (int r = 0; r < 16; ++r) v[r] += __uint_as_float(x[r]);
+          }
+#pragma unroll
+          for (int k = 0; k < kStep; ++k) {
+            const float w = __shfl_sync(0xffffffffu, f[t], rg + k);
+            const float y = w == 0.0f ? 0.0f : v[k] * w;
+            o[k] = t == 0 ? y : o[k] + y;
+          }
         }
         if (bad != 0u) {     // query i sees the boundary keys 0..i-1
           int i = (row0 + rg) % a.Nq;
