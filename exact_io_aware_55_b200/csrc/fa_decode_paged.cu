@@ -58,6 +58,7 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
+constexpr float kNoKey = 3.0e38f;
 constexpr float kBase = 1024.0f;            // P is scaled by 2^10: below 2^15, of e5m2's 57344
 
 template <int D, int R>
@@ -80,12 +81,12 @@ struct PgShape {
   static constexpr int kQRows = 2 * R;                        // hi, lo
   static constexpr int kQBytes = kQRows * D;
   static constexpr int kPRows = (R == 8) ? 32 : 3 * R;        // hi, mid, lo (and zero rows up to a multiple of 16)
-  static constexpr int kPSub = kPRows * 128;                  // P^T of one sub-tile
-  static constexpr int kPBytes = kSub * kPSub;
+  static constexpr int kPChunk = kTileKeys * 16;              // 16 rows of P^T for every key
+  static constexpr int kPBytes = kPRows / 16 * kPChunk;
   static constexpr int kKSteps = D / 32;                      // S^T k-steps per sub-tile
   static constexpr int kPvSteps = kTileKeys / 32;             // O^T k-steps per tile
   static constexpr uint32_t kIdS = idesc_e4m3(128, kQRows, false, false);
-  static constexpr uint32_t kIdO = idesc_e4m3(D, kPRows, true, false) | (1u << 10);   // B format 1: e5m2
+  static constexpr uint32_t kIdO = idesc_e4m3(D, kPRows, true, true) | (1u << 10);    // B format 1: e5m2
   static constexpr uint32_t kColS = 0;                        // kBufs S^T buffers of kQRows * kSub columns
   static constexpr uint32_t kColO = kBufs * kQRows * kSub;        // two O^T buffers of kPRows columns per turn
   static constexpr uint32_t kCols = kColO + 2 * kTurns * kPRows;
@@ -140,6 +141,11 @@ __device__ __forceinline__ uint64_t pg_desc(uint32_t saddr) {
   uint64_t d = sdesc_sw128(saddr, 16, 8 * D);
   if (D == 64) d = (d & ~(uint64_t(7) << 61)) | (uint64_t(4) << 61);   // 64-byte swizzle
   return d;
+}
+// P^T without swizzle: 8 keys x 16 rows in 128 bytes, a key's 16 rows together;
+// 8-key groups follow one another, chunks of 16 rows are `chunk` bytes apart.
+__device__ __forceinline__ uint64_t pg_desc_p(uint32_t saddr, uint32_t chunk) {
+  return sdesc_sw128(saddr, 128, chunk) & ~(uint64_t(7) << 61);
 }
 // 16-byte unit `c` of row `row` in that layout, as a byte offset.
 template <int D>
@@ -570,8 +576,8 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     for (int i = threadIdx.x - 32 * S::kEpi; i < 256; i += 128) b->nan_keys[i >> 7][i & 127] = 0u;
   }
   if (R == 8 && warp >= 4 && warp < 8) {             // the zero rows of P^T
-    for (int i = threadIdx.x - 128; i < 2 * U * 64; i += 128)
-      *reinterpret_cast<uint4*>(sP + (i >> 6) * S::kPSub + 24 * 128 + (i & 63) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x - 128; i < 2 * TILE; i += 128)
+      *reinterpret_cast<uint2*>(sP + i / TILE * S::kPBytes + S::kPChunk + i % TILE * 16 + 8) = make_uint2(0u, 0u);
     fence_proxy_async_smem();
   }
   // What came before in the stream may have written any of the inputs.
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------------ PV
     const uint64_t dV = pg_desc<D>(smem_u32(sKV + S::kTileBytes));              // V tiles, MN-major (A)
-    const uint64_t dP = sdesc_sw128(smem_u32(sP), 16, 1024);                    // P^T, K-major (B)
+    const uint64_t dP = pg_desc_p(smem_u32(sP), S::kPChunk);                    // P^T, MN-major (B)
     Walk<TILE> walk(a, start, n_tiles);
     Piece pc;
     int j = 0, n = 0;                                // tile of the piece, its tiles
@@ -710,7 +716,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 #pragma unroll
       for (int kt = 0; kt < S::kPvSteps; ++kt) {
         const uint64_t va = uint64_t((s * S::kStageBytes + kt * 32 * D) >> 4);
-        const uint64_t po = uint64_t((pb * S::kPBytes + (kt >> 2) * S::kPSub + (kt & 3) * 32) >> 4);
+        const uint64_t po = uint64_t((pb * S::kPBytes + kt * 512) >> 4);
         mma_f8_ss_e(col_o, dV + va, dP + po, S::kIdO, (!first || kt > 0) ? 1u : 0u);
       }
       tc_commit_e(&b->kv_empty[s]);                  // P is read with V, and O has the tile
@@ -792,10 +798,11 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     for (; walk.next(pc); ++it) {
       const int ob = it & 1, qb = it % S::kBufs;
       const int row0 = (a.row_tiles == 1 ? 0 : pc.unit % a.row_tiles) * R + hr;
-      float m_used[H], l_t[H];
+      // minus the maximum in use (of no key yet: any score lifts it), and the sum
+      float nm[H], l_t[H];
 #pragma unroll
       for (int r = 0; r < H; ++r) {
-        m_used[r] = -INFINITY;
+        nm[r] = kNoKey;
         l_t[r] = 0.0f;
       }
       bool began = false;                            // O holds a tile of this piece
@@ -831,12 +838,14 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < H; r += 4) {
             const float4 qf = *reinterpret_cast<const float4*>(&b->q_factor[qb][hr + r]);
-            s[u][r] = there ? fmaf(s[u][r], qf.x * f.x, f.y) : -INFINITY;
-            s[u][r + 1] = there ? fmaf(s[u][r + 1], qf.y * f.x, f.y) : -INFINITY;
-            s[u][r + 2] = there ? fmaf(s[u][r + 2], qf.z * f.x, f.y) : -INFINITY;
-            s[u][r + 3] = there ? fmaf(s[u][r + 3], qf.w * f.x, f.y) : -INFINITY;
+            s[u][r] = fmaf(s[u][r], qf.x * f.x, f.y);
+            s[u][r + 1] = fmaf(s[u][r + 1], qf.y * f.x, f.y);
+            s[u][r + 2] = fmaf(s[u][r + 2], qf.z * f.x, f.y);
+            s[u][r + 3] = fmaf(s[u][r + 3], qf.w * f.x, f.y);
           }
-          if (!there) {      // stale codes of V must not meet p = 0; each group clears its part of the row
+          if (!there) {      // stale codes: of K, whatever came of them; of V, they must not meet p = 0
+#pragma unroll
+            for (int r = 0; r < H; ++r) s[u][r] = -INFINITY;
             uint8_t* v = sKV + st * S::kStageBytes + S::kTileBytes + kt * D + part * (D / S::kSplit);
 #pragma unroll
             for (int c = 0; c < D / S::kSplit / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -869,7 +878,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < H; ++r)
 #pragma unroll
-          for (int u = 0; u < U; ++u) need |= s[u][r] > m_used[r] + kRescaleThreshold;
+          for (int u = 0; u < U; ++u) need |= s[u][r] + nm[r] > kRescaleThreshold;
         if (group_any(1 + group, need)) {
 #pragma unroll
           for (int r = 0; r < H; r += 4) {
@@ -895,8 +904,8 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
                                 fmaxf(fmaxf(x0.z, x1.z), fmaxf(x2.z, x3.z)), fmaxf(fmaxf(x0.w, x1.w), fmaxf(x2.w, x3.w))};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              before[r + k] = m_used[r + k];
-              m_used[r + k] = fmaxf(m_used[r + k], x[k]);
+              before[r + k] = nm[r + k];
+              nm[r + k] = fminf(nm[r + k], -x[k]);
             }
           }
           if (began) {   // rescale O^T, once the last product into it is done
@@ -905,7 +914,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             float alpha[H];
 #pragma unroll
             for (int r = 0; r < H; ++r) {
-              alpha[r] = m_used[r] == -INFINITY ? 1.0f : ex2_approx(before[r] - m_used[r]);
+              alpha[r] = ex2_approx(nm[r] - before[r]);
               l_t[r] *= alpha[r];
             }
             if (ok) {
@@ -922,40 +931,41 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             }
           }
         }
-        // P^T into shared memory: B operand, K-major, rows = parts of the query
-        // rows, the sub-tile's 128 keys in one 128-byte swizzled row.  The
-        // buffer is free once PV(g - 2) has read it, which gave its stage back.
+        // P^T into shared memory: B operand, MN-major, so that a key's eight rows
+        // of one part are eight bytes in one place.  The buffer is free once PV(g - 2) has read it, which gave its stage back.
         began = true;
         const int pb = g & 1;
         if (g >= 2) ok = ok && pg_wait(&b->kv_empty[(g - 2) % NS], ((g - 2) / NS) & 1, wc, WAIT_PAGED_PV);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int key = wq * 32 + lane;
-          uint8_t* pbase = sP + pb * S::kPBytes + u * S::kPSub + (key & 15) + hr * 128;
-          const int unit = key >> 4;
+          uint32_t hi[H / 2], mid[H / 2], lo[H / 2];
 #pragma unroll
           for (int r = 0; r < H; r += 2) {
-            const float p0 = (s[u][r] == -INFINITY) ? 0.0f : ex2_approx(s[u][r] - m_used[r]);
-            const float p1 = (s[u][r + 1] == -INFINITY) ? 0.0f : ex2_approx(s[u][r + 1] - m_used[r + 1]);
+            const float p0 = ex2_approx(s[u][r] + nm[r]), p1 = ex2_approx(s[u][r + 1] + nm[r + 1]);
             l_t[r] = fmaf(p0, inv[u], l_t[r]);
             l_t[r + 1] = fmaf(p1, inv[u], l_t[r + 1]);
             // p * vs in fp16, then its three e5m2 parts (e5m2 is fp16's upper
             // byte; adding 0x80 rounds the magnitude to nearest)
             const __half2 h = __floats2half2_rn(p0 * share[u], p1 * share[u]);
-            const uint32_t hi = (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xff00ff00u;
-            const __half2 d1 = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hi)), __float2half2_rn(8.0f));
-            const uint32_t mid = (*reinterpret_cast<const uint32_t*>(&d1) + 0x00800080u) & 0xff00ff00u;
-            const __half2 d2 = __hmul2(__hsub2(d1, *reinterpret_cast<const __half2*>(&mid)), __float2half2_rn(8.0f));
-            const uint32_t lo = *reinterpret_cast<const uint32_t*>(&d2) + 0x00800080u;
-            // hr is a multiple of 8: the swizzle goes by r
-            uint8_t* p_even = pbase + r * 128 + ((unit ^ (r & 7)) << 4);
-            uint8_t* p_odd = pbase + (r + 1) * 128 + ((unit ^ ((r + 1) & 7)) << 4);
-            p_even[0] = static_cast<uint8_t>(hi >> 8);
-            p_odd[0] = static_cast<uint8_t>(hi >> 24);
-            p_even[R * 128] = static_cast<uint8_t>(mid >> 8);
-            p_odd[R * 128] = static_cast<uint8_t>(mid >> 24);
-            p_even[2 * R * 128] = static_cast<uint8_t>(lo >> 8);
-            p_odd[2 * R * 128] = static_cast<uint8_t>(lo >> 24);
+            hi[r / 2] = (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xff00ff00u;
+            const __half2 d1 = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hi[r / 2])), __float2half2_rn(8.0f));
+            mid[r / 2] = (*reinterpret_cast<const uint32_t*>(&d1) + 0x00800080u) & 0xff00ff00u;
+            const __half2 d2 = __hmul2(__hsub2(d1, *reinterpret_cast<const __half2*>(&mid[r / 2])), __float2half2_rn(8.0f));
+            lo[r / 2] = *reinterpret_cast<const uint32_t*>(&d2) + 0x00800080u;
+          }
+          // the upper bytes of eight rows together
+          const uint2 h8 = make_uint2(__byte_perm(hi[0], hi[1], 0x7531), __byte_perm(hi[2], hi[3], 0x7531));
+          const uint2 m8 = make_uint2(__byte_perm(mid[0], mid[1], 0x7531), __byte_perm(mid[2], mid[3], 0x7531));
+          const uint2 l8 = make_uint2(__byte_perm(lo[0], lo[1], 0x7531), __byte_perm(lo[2], lo[3], 0x7531));
+          uint8_t* dst = sP + pb * S::kPBytes + (128 * u + wq * 32 + lane) * 16;
+          if constexpr (R == 8) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(h8.x, h8.y, m8.x, m8.y);
+            *reinterpret_cast<uint2*>(dst + S::kPChunk) = l8;
+          } else {
+            uint8_t* at = dst + hr / 16 * S::kPChunk + (hr & 8);
+            *reinterpret_cast<uint2*>(at) = h8;
+            *reinterpret_cast<uint2*>(at + R / 16 * S::kPChunk) = m8;
+            *reinterpret_cast<uint2*>(at + R / 8 * S::kPChunk) = l8;
           }
         }
         fence_proxy_async_smem();
@@ -975,7 +985,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         if (wq == 0 && lane == 0) {
           // scores that are all NaN leave no maximum, but a sum to be seen
 #pragma unroll
-          for (int r = 0; r < H; ++r) b->stat_m[ob][turn][hr + r] = m_used[r] == -INFINITY && l_t[r] != l_t[r] ? 0.0f : m_used[r];
+          for (int r = 0; r < H; ++r) b->stat_m[ob][turn][hr + r] = nm[r] < kNoKey ? -nm[r] : l_t[r] == l_t[r] ? -INFINITY : 0.0f;
         }
       } else if (ok && wq == 0 && lane < H) {
         b->stat_m[ob][turn][hr + lane] = -INFINITY;  // no tile of the piece: the sums are not looked at
