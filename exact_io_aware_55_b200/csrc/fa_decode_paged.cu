@@ -22,10 +22,9 @@
 //                   fp16's exponent range, so a key down to 2^-28 of the largest
 //                   keeps its 11 bits.  A and B of one product may differ in
 //                   type among the 8-bit floats.
-// A page's K scale multiplies its keys' scores; the power of two in its V scale
-// is added to the score's exponent (t = s + e, P = exp2(t - m) * vs / 2^e), so
-// that the parts cannot overflow whatever the scales are, and l sums
-// exp2(t - m) / 2^e.
+// A page's K scale multiplies its keys' scores; its V scale goes into the
+// exponent (t = s + log2 vs, P = exp2(t - m)), so that the parts cannot overflow
+// whatever the scales are, and l sums exp2(t - m) / vs.
 //
 // Work.  A unit is (request, KV head, tile of up to R query rows); its keys are
 // cut into tiles of 128 (d = 128) or 256 (d = 64) tokens, 32 KB of codes.  The
@@ -58,8 +57,7 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
-constexpr float kNoKey = 3.0e38f;
-constexpr float kBase = 1024.0f;            // P is scaled by 2^10: below 2^15, of e5m2's 57344
+constexpr float kBaseExp = 11.0f, kBase = 2048.0f;   // P is scaled by 2^11: at most 2^15, of e5m2's 57344
 
 template <int D, int R>
 struct PgShape {
@@ -78,17 +76,23 @@ struct PgShape {
   static constexpr int kBufs = 2 * kTurns;                    // of S^T and of the queries
   static constexpr int kNS = (R == 32 || (D == 64 && R == 16)) ? 5 : 6;   // ring depth: 160 or 192 KB
   static constexpr int kMaxPages = kTileKeys / 16;
+  // The query's parts are columns of their own for 8 rows (a product has 16
+  // columns at least), with 16 times the low part; from 16 rows on both products
+  // go into the same columns, with the low part as it is.
+  static constexpr bool kFold = R >= 16;
+  static constexpr float kLoScale = kFold ? 1.0f : 16.0f;
   static constexpr int kQRows = 2 * R;                        // hi, lo
+  static constexpr int kSCols = kFold ? R : 2 * R;
   static constexpr int kQBytes = kQRows * D;
   static constexpr int kPRows = (R == 8) ? 32 : 3 * R;        // hi, mid, lo (and zero rows up to a multiple of 16)
   static constexpr int kPChunk = kTileKeys * 16;              // 16 rows of P^T for every key
   static constexpr int kPBytes = kPRows / 16 * kPChunk;
   static constexpr int kKSteps = D / 32;                      // S^T k-steps per sub-tile
   static constexpr int kPvSteps = kTileKeys / 32;             // O^T k-steps per tile
-  static constexpr uint32_t kIdS = idesc_e4m3(128, kQRows, false, false);
+  static constexpr uint32_t kIdS = idesc_e4m3(128, kSCols, false, false);
   static constexpr uint32_t kIdO = idesc_e4m3(D, kPRows, true, true) | (1u << 10);    // B format 1: e5m2
-  static constexpr uint32_t kColS = 0;                        // kBufs S^T buffers of kQRows * kSub columns
-  static constexpr uint32_t kColO = kBufs * kQRows * kSub;        // two O^T buffers of kPRows columns per turn
+  static constexpr uint32_t kColS = 0;                        // kBufs S^T buffers of kSCols * kSub columns
+  static constexpr uint32_t kColO = kBufs * kSCols * kSub;        // two O^T buffers of kPRows columns per turn
   static constexpr uint32_t kCols = kColO + 2 * kTurns * kPRows;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "TMEM columns");
@@ -112,7 +116,7 @@ struct PgBarriers {
   uint64_t o_full[2], o_free[2];
   uint64_t stats_full[2];
   uint64_t merged;
-  alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, e, 2^-e, vs / 2^e
+  alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, 11 + log2 vs, 2^-11 / vs, 0 if vs is
   alignas(16) float q_factor[BUFS][R];        // power of two that a row of queries was divided by
   alignas(16) float red_max[TURNS][4][R];  // per-warp tile maxima (log2 units)
   alignas(16) float stat_m[2][TURNS][R];     // piece's running max
@@ -264,13 +268,13 @@ __device__ __forceinline__ float rows_sum(const float (&x)[H], int lane) {
 __device__ __forceinline__ int kv_head(const PagedArgs& a, int unit) { return a.row_tiles == 1 ? unit : unit / a.row_tiles; }
 
 // Two bf16 queries times `inv` (below 256) as two e4m3 parts each: the value
-// rounded, and 16 times what is left of it.
-__device__ __forceinline__ void split_pair(uint32_t q, float inv, uint32_t& hi, uint32_t& lo) {
+// rounded, and `lo_scale` times what is left of it.
+__device__ __forceinline__ void split_pair(uint32_t q, float inv, float lo_scale, uint32_t& hi, uint32_t& lo) {
   const float x = __uint_as_float(q << 16) * inv, y = __uint_as_float(q & 0xffff0000u) * inv;
   hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  lo = __nv_cvt_float2_to_fp8x2(make_float2((x - f.x) * 16.0f, (y - f.y) * 16.0f), __NV_SATFINITE, __NV_E4M3);
+  lo = __nv_cvt_float2_to_fp8x2(make_float2((x - f.x) * lo_scale, (y - f.y) * lo_scale), __NV_SATFINITE, __NV_E4M3);
 }
 
 __device__ __forceinline__ int pg_len(const PagedArgs& a, int b) { return min(max(a.seq_lens[b], 0), a.max_pages * a.page); }
@@ -340,7 +344,7 @@ struct QueryRows {
       const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) split_pair(x[k], inv, hi[k], lo[k]);
+      for (int k = 0; k < 4; ++k) split_pair(x[k], inv, PgShape<D, R>::kLoScale, hi[k], lo[k]);
       const int place = (lane & 3) * (D / 64) + (c >> 1);
       *reinterpret_cast<uint2*>(dst + pg_unit<D>(r, place) + (c & 1) * 8) =
           make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
@@ -687,7 +691,9 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         for (int ks = 0; ks < S::kKSteps; ++ks) {
           const uint64_t ka = uint64_t((s * S::kStageBytes + u * 128 * D + ks * 32) >> 4);
           const uint64_t qo = uint64_t((qb * S::kQBytes + ks * 32) >> 4);
-          mma_f8_ss_e(tmem + S::kColS + S::kQRows * (sb * U + u), dK + ka, dQ + qo, S::kIdS, ks > 0 ? 1u : 0u);
+          const uint32_t col = tmem + S::kColS + S::kSCols * (sb * U + u);
+          mma_f8_ss_e(col, dK + ka, dQ + qo, S::kIdS, ks > 0 ? 1u : 0u);
+          if (S::kFold) mma_f8_ss_e(col, dK + ka, dQ + qo + uint64_t((R * D) >> 4), S::kIdS, 1u);
         }
       tc_commit_e(&b->s_full[sb]);
       if (--left == 0) tc_commit_e(&b->q_empty[qb]);
@@ -737,10 +743,8 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     for (int t0 = 0; t0 < n_tiles && ok; t0 += pb.tiles) {
       const int next = pb.fetch();
       const int m = min(pb.tiles, n_tiles - t0);
-      // the exponent takes vs's power of two (2^-60 for 0 and what is smaller), P the rest
-      const int e = min(max(static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 127, -60), 100);
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      const float4 f = row >= 0 ? make_float4(ks * a.c_log2, static_cast<float>(e), inv, vs * inv * kBase)
+      const float v = fmaxf(vs, 8.673617379884035e-19f);     // 2^-60; the values of a scale of 0 are cleared
+      const float4 f = row >= 0 ? make_float4(ks * a.c_log2, log2f(v) + kBaseExp, (1.0f / kBase) / v, vs)
                                 : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
       for (int u = 0; u < m; ++u) {
         if (left == 0) {
@@ -798,13 +802,11 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     for (; walk.next(pc); ++it) {
       const int ob = it & 1, qb = it % S::kBufs;
       const int row0 = (a.row_tiles == 1 ? 0 : pc.unit % a.row_tiles) * R + hr;
-      // minus the maximum in use (of no key yet: any score lifts it), and the sum
+      // minus the maximum in use, the sum, and the rows that have a maximum
       float nm[H], l_t[H];
+      uint32_t have = 0;
 #pragma unroll
-      for (int r = 0; r < H; ++r) {
-        nm[r] = kNoKey;
-        l_t[r] = 0.0f;
-      }
+      for (int r = 0; r < H; ++r) nm[r] = l_t[r] = 0.0f;
       bool began = false;                            // O holds a tile of this piece
       for (int j = 0; j < pc.n; ++j, ++g) {
         if (g % S::kTurns != turn) continue;
@@ -814,38 +816,43 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
                             (g / S::kBufs) & 1, wc, WAIT_PAGED_S);
         tc_fence_after();
         const int tile0 = (pc.j0 + j) * TILE;
-        float s[U][H];
-        float inv[U], share[U];
+        float s[U][H], inv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const uint32_t col = lane_base + S::kColS + S::kQRows * (sb * U + u) + hr;
+          const uint32_t col = lane_base + S::kColS + S::kSCols * (sb * U + u) + hr;
           uint32_t x[H], y[H];
-          tmem_ld2<H>(col, col + R, x, y);
+          if constexpr (S::kFold) {
+            tmem_ld<H>(col, x);
 #pragma unroll
-          for (int r = 0; r < H; ++r) s[u][r] = fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r]));
+            for (int r = 0; r < H; ++r) s[u][r] = __uint_as_float(x[r]);
+          } else {
+            tmem_ld2<H>(col, col + R, x, y);
+#pragma unroll
+            for (int r = 0; r < H; ++r) s[u][r] = fmaf(__uint_as_float(y[r]), 1.0f / S::kLoScale, __uint_as_float(x[r]));
+          }
         }
         tc_fence_before();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&b->s_free[sb]);
-        bool need = false;
+        // s becomes the exponent of P, 11 + t - m
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int kt = 128 * u + wq * 32 + lane;
           const float4 f = b->page[st][kt >> page_shift];
           inv[u] = f.z;
-          share[u] = f.w;
           const bool there = tile0 + kt < pc.len && f.y != -INFINITY;
 #pragma unroll
           for (int r = 0; r < H; r += 4) {
             const float4 qf = *reinterpret_cast<const float4*>(&b->q_factor[qb][hr + r]);
-            s[u][r] = fmaf(s[u][r], qf.x * f.x, f.y);
-            s[u][r + 1] = fmaf(s[u][r + 1], qf.y * f.x, f.y);
-            s[u][r + 2] = fmaf(s[u][r + 2], qf.z * f.x, f.y);
-            s[u][r + 3] = fmaf(s[u][r + 3], qf.w * f.x, f.y);
+            s[u][r] = fmaf(s[u][r], qf.x * f.x, f.y + nm[r]);
+            s[u][r + 1] = fmaf(s[u][r + 1], qf.y * f.x, f.y + nm[r + 1]);
+            s[u][r + 2] = fmaf(s[u][r + 2], qf.z * f.x, f.y + nm[r + 2]);
+            s[u][r + 3] = fmaf(s[u][r + 3], qf.w * f.x, f.y + nm[r + 3]);
           }
-          if (!there) {      // stale codes: of K, whatever came of them; of V, they must not meet p = 0
+          if (!there)        // whatever came of stale codes
 #pragma unroll
             for (int r = 0; r < H; ++r) s[u][r] = -INFINITY;
+          if (!there || f.w == 0.0f) {   // of V, they must not meet p = 0
             uint8_t* v = sKV + st * S::kStageBytes + S::kTileBytes + kt * D + part * (D / S::kSplit);
 #pragma unroll
             for (int c = 0; c < D / S::kSplit / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -873,12 +880,13 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           }
         }
         // Does any key of the tile lift a row's maximum by more than the
-        // threshold?  One barrier with a vote; the maxima themselves are only
-        // exchanged when one does.
+        // threshold, or has a row none yet?  One barrier with a vote; the maxima
+        // themselves are only exchanged when one does.
+        bool need = have != (1u << H) - 1u;
 #pragma unroll
         for (int r = 0; r < H; ++r)
 #pragma unroll
-          for (int u = 0; u < U; ++u) need |= s[u][r] + nm[r] > kRescaleThreshold;
+          for (int u = 0; u < U; ++u) need |= s[u][r] > kBaseExp + kRescaleThreshold;
         if (group_any(1 + group, need)) {
 #pragma unroll
           for (int r = 0; r < H; r += 4) {
@@ -893,7 +901,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             if (lane == 0) *reinterpret_cast<float4*>(&b->red_max[turn][wq][hr + r]) = make_float4(x[0], x[1], x[2], x[3]);
           }
           group_sync(1 + group);
-          float before[H];
+          float alpha[H];
 #pragma unroll
           for (int r = 0; r < H; r += 4) {
             const float4 x0 = *reinterpret_cast<const float4*>(&b->red_max[turn][0][hr + r]);
@@ -904,19 +912,22 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
                                 fmaxf(fmaxf(x0.z, x1.z), fmaxf(x2.z, x3.z)), fmaxf(fmaxf(x0.w, x1.w), fmaxf(x2.w, x3.w))};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              before[r + k] = nm[r + k];
-              nm[r + k] = fminf(nm[r + k], -x[k]);
+              // the first maximum is taken as it is, later ones only rise
+              const bool first = !((have >> (r + k)) & 1u);
+              const float up = x[k] - kBaseExp;
+              const float shift = x[k] == -INFINITY ? 0.0f : first ? up : fmaxf(up, 0.0f);
+              alpha[r + k] = first ? 1.0f : ex2_approx(-shift);
+              nm[r + k] -= shift;
+#pragma unroll
+              for (int u = 0; u < U; ++u) s[u][r + k] -= shift;
+              if (x[k] != -INFINITY) have |= 1u << (r + k);
             }
           }
           if (began) {   // rescale O^T, once the last product into it is done
             ok = ok && pg_wait(&b->kv_empty[(g - S::kTurns) % NS], ((g - S::kTurns) / NS) & 1, wc, WAIT_PAGED_PV);
             tc_fence_after();
-            float alpha[H];
 #pragma unroll
-            for (int r = 0; r < H; ++r) {
-              alpha[r] = ex2_approx(nm[r] - before[r]);
-              l_t[r] *= alpha[r];
-            }
+            for (int r = 0; r < H; ++r) l_t[r] *= alpha[r];
             if (ok) {
 #pragma unroll
               for (int k = 0; k < 3; ++k) {
@@ -941,12 +952,12 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           uint32_t hi[H / 2], mid[H / 2], lo[H / 2];
 #pragma unroll
           for (int r = 0; r < H; r += 2) {
-            const float p0 = ex2_approx(s[u][r] + nm[r]), p1 = ex2_approx(s[u][r + 1] + nm[r + 1]);
+            const float p0 = ex2_approx(s[u][r]), p1 = ex2_approx(s[u][r + 1]);
             l_t[r] = fmaf(p0, inv[u], l_t[r]);
             l_t[r + 1] = fmaf(p1, inv[u], l_t[r + 1]);
-            // p * vs in fp16, then its three e5m2 parts (e5m2 is fp16's upper
+            // in fp16, then its three e5m2 parts (e5m2 is fp16's upper
             // byte; adding 0x80 rounds the magnitude to nearest)
-            const __half2 h = __floats2half2_rn(p0 * share[u], p1 * share[u]);
+            const __half2 h = __floats2half2_rn(p0, p1);
             hi[r / 2] = (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xff00ff00u;
             const __half2 d1 = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hi[r / 2])), __float2half2_rn(8.0f));
             mid[r / 2] = (*reinterpret_cast<const uint32_t*>(&d1) + 0x00800080u) & 0xff00ff00u;
@@ -985,7 +996,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         if (wq == 0 && lane == 0) {
           // scores that are all NaN leave no maximum, but a sum to be seen
 #pragma unroll
-          for (int r = 0; r < H; ++r) b->stat_m[ob][turn][hr + r] = nm[r] < kNoKey ? -nm[r] : l_t[r] == l_t[r] ? -INFINITY : 0.0f;
+          for (int r = 0; r < H; ++r) b->stat_m[ob][turn][hr + r] = (have >> r) & 1u ? -nm[r] : l_t[r] == l_t[r] ? -INFINITY : 0.0f;
         }
       } else if (ok && wq == 0 && lane < H) {
         b->stat_m[ob][turn][hr + lane] = -INFINITY;  // no tile of the piece: the sums are not looked at
