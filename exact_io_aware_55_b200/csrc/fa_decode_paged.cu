@@ -29,8 +29,8 @@
 // Work.  A unit is (request, KV head, tile of up to R query rows); its keys are
 // cut into tiles of 128 (d = 128) or 256 (d = 64) tokens, 32 KB of codes.  The
 // lengths are known on the device only, so every CTA adds them up itself and
-// takes an equal share of all tiles, a contiguous range that may begin and end
-// inside a unit.  A unit that lies within one CTA is written directly; of a
+// takes an equal share of all tiles (a unit counts for two more), a contiguous
+// range that may begin and end inside a unit.  A unit that lies within one CTA is written directly; of a
 // unit cut between CTAs each CTA leaves its normalised O and LSE in one of its
 // two slots of the workspace (one for a piece that does not begin its unit, one
 // for a piece that does), and the CTA that is the last to finish a piece of the
@@ -56,6 +56,9 @@ namespace fa {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
+// What a piece costs beside its tiles, in tiles (measured: a batch of 256 x 512
+// keys takes 72 us with 0, XX with 2).
+constexpr int kPieceCost = 2;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
 constexpr float kBaseExp = 11.0f, kBase = 2048.0f;   // P is scaled by 2^11: at most 2^15, of e5m2's 57344
 
@@ -122,7 +125,8 @@ struct PgBarriers {
   alignas(16) float stat_m[2][TURNS][R];     // piece's running max
   alignas(16) float stat_l[2][TURNS][4][R];  // piece's per-warp sums
   uint32_t nan_keys[2][128];               // per column of a piece: boundary keys whose V code is NaN
-  int per, n_tiles;
+  long long first_tile[2];                 // of this CTA's share and of the next
+  int per, start_rest;                     // length of a share; how far into a unit's line it begins
   int n_merge;                             // units that this CTA is the last to have finished a piece of
   Merge merge[2];
   Place start;
@@ -586,39 +590,58 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
   }
   // What came before in the stream may have written any of the inputs.
   grid_dependency_wait();
-  // This CTA's share of all tiles, and the place where it begins.  Tiles of one
-  // KV head are summed in 32 bits (there are fewer than table entries).
+  // This CTA's share of all tiles, and the place where it begins.  The units
+  // are laid on one line, each kPieceCost and a step per tile long; a CTA has the
+  // tiles in its equal part of the line.  One KV head's tiles, and its length of
+  // line, are summed in 32 bits (there are fewer tiles than table entries).
   if (warp == 0) {
     const int chunk = (a.B + 31) >> 5;
     const int c0 = min(a.B, lane * chunk), c1 = min(a.B, c0 + chunk);
-    unsigned mine = 0;
+    unsigned long long mine = 0;                     // length of line, number of tiles
 #pragma unroll 4
-    for (int i = c0; i < c1; ++i) mine += (pg_len(a, i) + TILE - 1) / TILE;
-    unsigned upto = mine;
+    for (int i = c0; i < c1; ++i) {
+      const unsigned nt = (pg_len(a, i) + TILE - 1) / TILE;
+      mine += (static_cast<unsigned long long>(nt > 0 ? nt + kPieceCost : 0) << 32) + nt;
+    }
+    unsigned long long upto = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-      const unsigned y = __shfl_up_sync(0xffffffffu, upto, m);
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, m);
       if (lane >= m) upto += y;
     }
-    const long long total = static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * a.units;
+    const unsigned long long sums = __shfl_sync(0xffffffffu, upto, 31);
+    const long long total = static_cast<long long>(sums >> 32) * a.units;
     const int per = static_cast<int>((static_cast<unsigned long long>(total) + kPagedCtas - 1) / kPagedCtas);
-    const long long g0 = min(total, static_cast<long long>(blockIdx.x) * per);
-    const int n = static_cast<int>(min(total - g0, static_cast<long long>(per)));
-    long long first = static_cast<long long>(upto - mine) * a.units;
-    if (n > 0 && first <= g0 && g0 < first + static_cast<long long>(mine) * a.units) {
-      int i = c0, len = pg_len(a, c0), nt = (len + TILE - 1) / TILE;
-      while (g0 >= first + static_cast<long long>(nt) * a.units) {
-        first += static_cast<long long>(nt) * a.units;
-        len = pg_len(a, ++i);
-        nt = (len + TILE - 1) / TILE;
-      }
-      const unsigned pos = static_cast<unsigned>(g0 - first), unit = pos / static_cast<unsigned>(nt);
-      b->start = Place{i, static_cast<int>(unit), static_cast<int>(pos - unit * nt), len, nt};
-    }
+    const long long x0 = static_cast<long long>(blockIdx.x) * per;
+    const long long line = static_cast<long long>((upto - mine) >> 32) * a.units;    // where this lane's requests begin
+    const long long tiles = static_cast<long long>(static_cast<unsigned>(upto - mine)) * a.units;
     if (lane == 0) {
       b->per = per;
-      b->n_tiles = n;
       b->n_merge = 0;
+      b->first_tile[0] = b->first_tile[1] = static_cast<long long>(static_cast<unsigned>(sums)) * a.units;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {                    // the first tile of this share and that of the next
+      const long long x = x0 + (k == 0 ? 0 : per);
+      if (line <= x && x < line + static_cast<long long>(mine >> 32) * a.units) {
+        long long at = line, t = tiles;
+        int i = c0, len = pg_len(a, c0), nt = (len + TILE - 1) / TILE;
+        while (nt == 0 || x >= at + static_cast<long long>(nt + kPieceCost) * a.units) {
+          if (nt > 0) at += static_cast<long long>(nt + kPieceCost) * a.units;
+          t += static_cast<long long>(nt) * a.units;
+          len = pg_len(a, ++i);
+          nt = (len + TILE - 1) / TILE;
+        }
+        const unsigned off = static_cast<unsigned>(x - at), unit = off / static_cast<unsigned>(nt + kPieceCost);
+        const int rest = static_cast<int>(off - unit * (nt + kPieceCost));
+        const int j = max(rest - kPieceCost, 0);
+        b->first_tile[k] = t + static_cast<long long>(unit) * nt + j;
+        if (k == 0) {
+          b->start = Place{i, static_cast<int>(unit), j, len, nt};
+          b->start_rest = rest;
+        }
+      }
     }
   }
   tc_fence_before();
@@ -626,7 +649,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = b->tmem_base;
   const Place start = b->start;
-  const int per = b->per, n_tiles = b->n_tiles;
+  const int per = b->per, n_tiles = static_cast<int>(b->first_tile[1] - b->first_tile[0]);
 
   if (n_tiles == 0) {
     // nothing but the empty requests below
@@ -1013,11 +1036,14 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     const int drow = (D == 128) ? wq * 32 + lane : (lane < 16 ? wq * 16 + lane : -1);
     Walk<TILE> walk(a, start, n_tiles);
     Piece pc;
+    int unit_at = -b->start_rest;                    // where the unit's line begins, from this CTA's part on
     bool ok = true;          // as for the softmax warps, for the barrier of cut pieces
     for (int it = 0; walk.next(pc); ++it) {
       const int ob = it & 1;
       ok = ok && pg_wait(&b->stats_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_STATS);
       const bool whole = pc.n == pc.nt;
+      const int began = unit_at;                     // tile j of the unit is at began + kPieceCost + j
+      if (pc.j0 + pc.n == pc.nt) unit_at += pc.nt + kPieceCost;
       const int slot = 2 * blockIdx.x + (pc.j0 > 0 ? 0 : 1);
       const int hk = kv_head(a, pc.unit);
       const int row0 = (pc.unit - hk * a.row_tiles) * R;
@@ -1112,9 +1138,10 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&b->o_free[ob]);
       if (!whole) {
-        // the unit's CTAs: each has per tiles, so the first began ceil(j0 / per) shares before
-        const int c0 = static_cast<int>(blockIdx.x) - (pc.j0 + per - 1) / per;
-        const int c1 = static_cast<int>(blockIdx.x) + (pc.nt - pc.j0 - pc.n + per - 1) / per;
+        // the CTAs whose parts of the line its first and last tile are in
+        const int to = began + kPieceCost;           // this CTA's part is 0..per - 1
+        const int c0 = static_cast<int>(blockIdx.x) - (pc.j0 > 0 ? (per - 1 - to) / per : 0);
+        const int c1 = static_cast<int>(blockIdx.x) + (to + pc.nt - 1) / per;
         group_sync(1 + S::kGroups);
         if (ok && warp == S::kEpi && mark_done(a.marks, a.nonce, slot, c0, c1, lane) && lane == 0)
           b->merge[b->n_merge++] = Merge{pc.b, pc.unit, c0, c1};
