@@ -77,7 +77,8 @@ struct PgShape {
   static constexpr int kTileBytes = kTileKeys * D;            // K (or V) codes of one tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kBufs = 2 * kTurns;                    // of S^T and of the queries
-  static constexpr int kNS = (R == 32 || (D == 64 && R == 16)) ? 5 : 6;   // ring depth: 160 or 192 KB
+  // Ring depth: a stage is K, V and P of a tile, 32 KB and kPBytes.
+  static constexpr int kNS = R == 8 ? 5 : R == 16 ? (D == 128 ? 5 : 4) : (D == 128 ? 4 : 3);
   static constexpr int kMaxPages = kTileKeys / 16;
   // The query's parts are columns of their own for 8 rows (a product has 16
   // columns at least), with 16 times the low part; from 16 rows on both products
@@ -112,10 +113,9 @@ struct Place {
 
 template <int R, int NS, int PAGES, int TURNS, int BUFS>
 struct PgBarriers {
-  uint64_t kv_full[NS], kv_empty[NS];
+  uint64_t kv_full[NS], kv_empty[NS], p_full[NS];
   uint64_t q_full[BUFS], q_empty[BUFS];
   uint64_t s_full[BUFS], s_free[BUFS];
-  uint64_t p_full[2];
   uint64_t o_full[2], o_free[2];
   uint64_t stats_full[2];
   uint64_t merged;
@@ -140,7 +140,7 @@ using PgBar = PgBarriers<R, PgShape<D, R>::kNS, PgShape<D, R>::kMaxPages, PgShap
 template <int D, int R>
 constexpr size_t pg_smem_bytes() {
   using S = PgShape<D, R>;
-  return 1024 + size_t(S::kNS) * S::kStageBytes + S::kBufs * S::kQBytes + 2 * S::kPBytes + sizeof(PgBar<D, R>);
+  return 1024 + size_t(S::kNS) * (S::kStageBytes + S::kPBytes) + S::kBufs * S::kQBytes + sizeof(PgBar<D, R>);
 }
 
 // Shared-memory matrix descriptor: rows of D bytes, swizzled over D bytes.
@@ -466,7 +466,7 @@ __device__ __forceinline__ void merge_unit(const PagedArgs& a, const Merge& u, u
                                            const WaitCtx& wc) {
   using S = PgShape<D, R>;
   constexpr int kVec = D / 32;                       // columns per lane
-  constexpr int kRing = S::kNS * S::kStageBytes + 2 * S::kPBytes;
+  constexpr int kRing = S::kNS * (S::kStageBytes + S::kPBytes);
   constexpr int kLse = kPagedCtas * R * 4;           // every piece's LSE comes first
   constexpr int kBatch = (kRing - kLse) / (R * D * 4);
   static_assert(kBatch >= 8, "pieces at a time");
@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;                               // NS x (K tile, V tile)
-  uint8_t* sP = sKV + NS * S::kStageBytes;           // 2 x P^T
-  uint8_t* sQ = sP + 2 * S::kPBytes;                 // kBufs x (hi, lo) queries
+  uint8_t* sP = sKV + NS * S::kStageBytes;           // NS x P^T
+  uint8_t* sQ = sP + NS * S::kPBytes;                 // kBufs x (hi, lo) queries
   auto* b = reinterpret_cast<PgBar<D, R>*>(sQ + S::kBufs * S::kQBytes);
   const WaitCtx wc{&b->abort, a.status, FA_WAIT_LIMIT_NS};
 
@@ -560,6 +560,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     if (lane < NS) {
       mbar_init(&b->kv_full[lane], 2);
       mbar_init(&b->kv_empty[lane], 1);
+      mbar_init(&b->p_full[lane], 4 * S::kSplit);
     }
     fence_mbar_init();
   } else if (warp == 3) {
@@ -570,7 +571,6 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       mbar_init(&b->s_free[lane], 4 * S::kSplit);
     }
     if (lane < 2) {
-      mbar_init(&b->p_full[lane], 4 * S::kSplit);
       mbar_init(&b->o_full[lane], 1);
       mbar_init(&b->o_free[lane], 4);
       mbar_init(&b->stats_full[lane], 4 * S::kGroups);
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     for (int i = threadIdx.x - 32 * S::kEpi; i < 256; i += 128) b->nan_keys[i >> 7][i & 127] = 0u;
   }
   if (R == 8 && warp >= 4 && warp < 8) {             // the zero rows of P^T
-    for (int i = threadIdx.x - 128; i < 2 * TILE; i += 128)
+    for (int i = threadIdx.x - 128; i < NS * TILE; i += 128)
       *reinterpret_cast<uint2*>(sP + i / TILE * S::kPBytes + S::kPChunk + i % TILE * 16 + 8) = make_uint2(0u, 0u);
     fence_proxy_async_smem();
   }
@@ -735,17 +735,17 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         j = 0;
         ++it;
       }
-      const int s = g % NS, pb = g & 1, ob = it & 1;
+      const int s = g % NS, ob = it & 1;
       const bool first = j < S::kTurns;              // into its turn's O
       const uint32_t col_o = tmem + S::kColO + S::kPRows * (S::kTurns * ob + g % S::kTurns);
       if ((j == 0 && it >= 2 && !pg_wait(&b->o_free[ob], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE)) ||
-          !pg_wait(&b->p_full[pb], (g >> 1) & 1, wc, WAIT_PAGED_P))
+          !pg_wait(&b->p_full[s], (g / NS) & 1, wc, WAIT_PAGED_P))
         break;
       tc_fence_after();
 #pragma unroll
       for (int kt = 0; kt < S::kPvSteps; ++kt) {
         const uint64_t va = uint64_t((s * S::kStageBytes + kt * 32 * D) >> 4);
-        const uint64_t po = uint64_t((pb * S::kPBytes + kt * 512) >> 4);
+        const uint64_t po = uint64_t((s * S::kPBytes + kt * 512) >> 4);
         mma_f8_ss_e(col_o, dV + va, dP + po, S::kIdO, (!first || kt > 0) ? 1u : 0u);
       }
       tc_commit_e(&b->kv_empty[s]);                  // P is read with V, and O has the tile
@@ -966,10 +966,9 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           }
         }
         // P^T into shared memory: B operand, MN-major, so that a key's eight rows
-        // of one part are eight bytes in one place.  The buffer is free once PV(g - 2) has read it, which gave its stage back.
+        // of one part are eight bytes in one place.  The buffer is the stage's: K
+        // could only come into it once the tile before had been read, P included.
         began = true;
-        const int pb = g & 1;
-        if (g >= 2) ok = ok && pg_wait(&b->kv_empty[(g - 2) % NS], ((g - 2) / NS) & 1, wc, WAIT_PAGED_PV);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           uint32_t hi[H / 2], mid[H / 2], lo[H / 2];
@@ -991,7 +990,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           const uint2 h8 = make_uint2(__byte_perm(hi[0], hi[1], 0x7531), __byte_perm(hi[2], hi[3], 0x7531));
           const uint2 m8 = make_uint2(__byte_perm(mid[0], mid[1], 0x7531), __byte_perm(mid[2], mid[3], 0x7531));
           const uint2 l8 = make_uint2(__byte_perm(lo[0], lo[1], 0x7531), __byte_perm(lo[2], lo[3], 0x7531));
-          uint8_t* dst = sP + pb * S::kPBytes + (128 * u + wq * 32 + lane) * 16;
+          uint8_t* dst = sP + st * S::kPBytes + (128 * u + wq * 32 + lane) * 16;
           if constexpr (R == 8) {
             *reinterpret_cast<uint4*>(dst) = make_uint4(h8.x, h8.y, m8.x, m8.y);
             *reinterpret_cast<uint2*>(dst + S::kPChunk) = l8;
@@ -1005,7 +1004,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&b->p_full[pb]);
+        if (ok && lane == 0) mbar_arrive(&b->p_full[st]);
       }
       // Piece done: publish the running max and the per-warp sums, once the
       // epilogue has let go of this buffer two pieces ago.  That every group had
