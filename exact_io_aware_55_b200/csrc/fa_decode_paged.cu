@@ -11,11 +11,11 @@
 // The codes therefore go from the pages straight to the tensor cores, as the
 // A operand of both products, and are never converted:
 //   S^T = K Q^T     keys x rows (M = 128 keys).  A bf16 query is the sum of two
-//                   e4m3 values: with the row scaled to |q| < 256, hi rounds to
-//                   4 bits and lo = 16 (q - hi) holds the other 4, so hi and lo
-//                   are two columns of the B operand and the scores are those
-//                   of the bf16 query (elements below 2^-10 of the row's
-//                   largest keep 2^-22 of it).
+//                   8-bit floats: with the row scaled to |q| < 256, hi rounds to
+//                   e4m3's 4 bits and lo is the rest, at most 8 of its last
+//                   steps.  Both multiply K, so the scores are those of the bf16
+//                   query (elements below 2^-10 of the row's largest, and far
+//                   below, keep 2^-21 of it).
 //   O^T += V^T P^T  d x rows (A = V tile, MN-major).  p * vs is rounded to fp16
 //                   and split into three e5m2 parts, hi + mid/8 + lo/64, which
 //                   is exact: 11 bits in three times 3 plus the signs.  e5m2 has
@@ -24,7 +24,9 @@
 //                   type among the 8-bit floats.
 // A page's K scale multiplies its keys' scores; its V scale goes into the
 // exponent (t = s + log2 vs, P = exp2(t - m)), so that the parts cannot overflow
-// whatever the scales are, and l sums exp2(t - m) / vs.
+// whatever the scales are, and l sums exp2(t - m) / vs.  t counts from a whole
+// number r near the log2 vs of the piece's first page, so that m and with it LSE
+// are no larger than the scores; O gets the factor 2^r at the end.
 //
 // Work.  A unit is (request, KV head, tile of up to R query rows); its keys are
 // cut into tiles of 128 (d = 128) or 256 (d = 64) tokens, 32 KB of codes.  The
@@ -60,7 +62,7 @@ constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 // keys takes 72 us with 0, XX with 2).
 constexpr int kPieceCost = 2;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
-constexpr float kBaseExp = 11.0f, kBase = 2048.0f;   // P is scaled by 2^11: at most 2^15, of e5m2's 57344
+constexpr float kBase = 2048.0f;            // P is scaled by 2^11: at most 2^15, of e5m2's 57344
 
 template <int D, int R>
 struct PgShape {
@@ -81,10 +83,10 @@ struct PgShape {
   static constexpr int kNS = R == 8 ? 5 : R == 16 ? (D == 128 ? 5 : 4) : (D == 128 ? 4 : 3);
   static constexpr int kMaxPages = kTileKeys / 16;
   // The query's parts are columns of their own for 8 rows (a product has 16
-  // columns at least), with 16 times the low part; from 16 rows on both products
-  // go into the same columns, with the low part as it is.
+  // columns at least), the low part 16 times itself; from 16 rows on both products
+  // go into the same columns, the low part as it is, in e5m2, whose range it needs.
   static constexpr bool kFold = R >= 16;
-  static constexpr float kLoScale = kFold ? 1.0f : 16.0f;
+  static constexpr float kLoScale = 16.0f;                    // where it is not folded
   static constexpr int kQRows = 2 * R;                        // hi, lo
   static constexpr int kSCols = kFold ? R : 2 * R;
   static constexpr int kQBytes = kQRows * D;
@@ -94,6 +96,7 @@ struct PgShape {
   static constexpr int kKSteps = D / 32;                      // S^T k-steps per sub-tile
   static constexpr int kPvSteps = kTileKeys / 32;             // O^T k-steps per tile
   static constexpr uint32_t kIdS = idesc_e4m3(128, kSCols, false, false);
+  static constexpr uint32_t kIdSLo = kIdS | (1u << 10);       // B format 1: e5m2
   static constexpr uint32_t kIdO = idesc_e4m3(D, kPRows, true, true) | (1u << 10);    // B format 1: e5m2
   static constexpr uint32_t kColS = 0;                        // kBufs S^T buffers of kSCols * kSub columns
   static constexpr uint32_t kColO = kBufs * kSCols * kSub;        // two O^T buffers of kPRows columns per turn
@@ -119,7 +122,9 @@ struct PgBarriers {
   uint64_t o_full[2], o_free[2];
   uint64_t stats_full[2];
   uint64_t merged;
-  alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, 11 + log2 vs, 2^-11 / vs, 0 if vs is
+  alignas(16) float4 page[NS][PAGES];      // per page of a tile: K factor, log2 vs - r, 2^r / vs, 0 if vs is
+  float page_ref[BUFS];                    // 2^r of a piece
+  float stat_ref[2];
   alignas(16) float q_factor[BUFS][R];        // power of two that a row of queries was divided by
   alignas(16) float red_max[TURNS][4][R];  // per-warp tile maxima (log2 units)
   alignas(16) float stat_m[2][TURNS][R];     // piece's running max
@@ -271,14 +276,16 @@ __device__ __forceinline__ float rows_sum(const float (&x)[H], int lane) {
 
 __device__ __forceinline__ int kv_head(const PagedArgs& a, int unit) { return a.row_tiles == 1 ? unit : unit / a.row_tiles; }
 
-// Two bf16 queries times `inv` (below 256) as two e4m3 parts each: the value
-// rounded, and `lo_scale` times what is left of it.
-__device__ __forceinline__ void split_pair(uint32_t q, float inv, float lo_scale, uint32_t& hi, uint32_t& lo) {
+// Two bf16 queries times `inv` (below 256) as two parts each: the value rounded
+// to e4m3, and what is left of it, in e5m2 (FOLD) or 16 times in e4m3.
+template <bool FOLD>
+__device__ __forceinline__ void split_pair(uint32_t q, float inv, uint32_t& hi, uint32_t& lo) {
   const float x = __uint_as_float(q << 16) * inv, y = __uint_as_float(q & 0xffff0000u) * inv;
   hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  lo = __nv_cvt_float2_to_fp8x2(make_float2((x - f.x) * lo_scale, (y - f.y) * lo_scale), __NV_SATFINITE, __NV_E4M3);
+  constexpr float k = FOLD ? 1.0f : 16.0f;
+  lo = __nv_cvt_float2_to_fp8x2(make_float2((x - f.x) * k, (y - f.y) * k), __NV_SATFINITE, FOLD ? __NV_E5M2 : __NV_E4M3);
 }
 
 __device__ __forceinline__ int pg_len(const PagedArgs& a, int b) { return min(max(a.seq_lens[b], 0), a.max_pages * a.page); }
@@ -348,7 +355,7 @@ struct QueryRows {
       const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) split_pair(x[k], inv, PgShape<D, R>::kLoScale, hi[k], lo[k]);
+      for (int k = 0; k < 4; ++k) split_pair<PgShape<D, R>::kFold>(x[k], inv, hi[k], lo[k]);
       const int place = (lane & 3) * (D / 64) + (c >> 1);
       *reinterpret_cast<uint2*>(dst + pg_unit<D>(r, place) + (c & 1) * 8) =
           make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
@@ -716,7 +723,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           const uint64_t qo = uint64_t((qb * S::kQBytes + ks * 32) >> 4);
           const uint32_t col = tmem + S::kColS + S::kSCols * (sb * U + u);
           mma_f8_ss_e(col, dK + ka, dQ + qo, S::kIdS, ks > 0 ? 1u : 0u);
-          if (S::kFold) mma_f8_ss_e(col, dK + ka, dQ + qo + uint64_t((R * D) >> 4), S::kIdS, 1u);
+          if (S::kFold) mma_f8_ss_e(col, dK + ka, dQ + qo + uint64_t((R * D) >> 4), S::kIdSLo, 1u);
         }
       tc_commit_e(&b->s_full[sb]);
       if (--left == 0) tc_commit_e(&b->q_empty[qb]);
@@ -762,13 +769,13 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     QueryRows<D> rows;
     rows.template load<R>(a, coming, 0, lane);
     int it = 0, left = 0;                            // pieces begun, tiles left of the last
+    float ref = 0.0f, ref2 = 1.0f;                   // r of the piece, 2^r
     bool ok = true;
     for (int t0 = 0; t0 < n_tiles && ok; t0 += pb.tiles) {
       const int next = pb.fetch();
       const int m = min(pb.tiles, n_tiles - t0);
       const float v = fmaxf(vs, 8.673617379884035e-19f);     // 2^-60; the values of a scale of 0 are cleared
-      const float4 f = row >= 0 ? make_float4(ks * a.c_log2, log2f(v) + kBaseExp, (1.0f / kBase) / v, vs)
-                                : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+      const float lv = log2f(v), iv = 1.0f / v;
       for (int u = 0; u < m; ++u) {
         if (left == 0) {
           pc = coming;
@@ -778,6 +785,10 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             ok = false;
             break;
           }
+          const float first_lv = __shfl_sync(0xffffffffu, row >= 0 && vs > 0.0f ? lv : 0.0f, u * pb.per_tile);
+          ref = fminf(fmaxf(rintf(first_lv), -100.0f), 100.0f);
+          ref2 = __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(ref)) << 23);
+          if (lane == 0) b->page_ref[qb] = ref2;
 #pragma unroll 1
           for (int first = 0;;) {
             rows.template split<R>(sQ + qb * S::kQBytes, b->q_factor[qb], first, lane);
@@ -798,7 +809,9 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           ok = false;
           break;
         }
-        if (pb.u == u) b->page[s][pb.i] = f;
+        if (pb.u == u)
+          b->page[s][pb.i] = row >= 0 ? make_float4(ks * a.c_log2, lv - ref, iv * ref2, vs)
+                                      : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->kv_full[s]);
       }
@@ -857,7 +870,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&b->s_free[sb]);
-        // s becomes the exponent of P, 11 + t - m
+        // s becomes the exponent of P, t - m
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int kt = 128 * u + wq * 32 + lane;
@@ -909,7 +922,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < H; ++r)
 #pragma unroll
-          for (int u = 0; u < U; ++u) need |= s[u][r] > kBaseExp + kRescaleThreshold;
+          for (int u = 0; u < U; ++u) need |= s[u][r] > kRescaleThreshold;
         if (group_any(1 + group, need)) {
 #pragma unroll
           for (int r = 0; r < H; r += 4) {
@@ -937,8 +950,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               // the first maximum is taken as it is, later ones only rise
               const bool first = !((have >> (r + k)) & 1u);
-              const float up = x[k] - kBaseExp;
-              const float shift = x[k] == -INFINITY ? 0.0f : first ? up : fmaxf(up, 0.0f);
+              const float shift = x[k] == -INFINITY ? 0.0f : first ? x[k] : fmaxf(x[k], 0.0f);
               alpha[r + k] = first ? 1.0f : ex2_approx(-shift);
               nm[r + k] -= shift;
 #pragma unroll
@@ -979,7 +991,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             l_t[r + 1] = fmaf(p1, inv[u], l_t[r + 1]);
             // in fp16, then its three e5m2 parts (e5m2 is fp16's upper
             // byte; adding 0x80 rounds the magnitude to nearest)
-            const __half2 h = __floats2half2_rn(p0, p1);
+            const __half2 h = __floats2half2_rn(p0 * kBase, p1 * kBase);
             hi[r / 2] = (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xff00ff00u;
             const __half2 d1 = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hi[r / 2])), __float2half2_rn(8.0f));
             mid[r / 2] = (*reinterpret_cast<const uint32_t*>(&d1) + 0x00800080u) & 0xff00ff00u;
@@ -1011,6 +1023,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       // left that piece is also why this one, which may have had no tile to wait
       // for in this piece, is not ahead of q_empty's phase.
       if (it >= 2) ok = ok && pg_wait(&b->o_free[ob], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE);
+      if (ok && group == 0 && wq == 0 && lane == 0) b->stat_ref[ob] = b->page_ref[qb];
       if (ok && lane == 0) mbar_arrive(&b->q_empty[qb]);
       if (ok && began) {
         const float l = rows_sum<H>(l_t, lane);      // of row lane / (32 / H)
@@ -1062,7 +1075,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           if (m != -INFINITY)
             L = fmaf(f[k], b->stat_l[ob][k][0][lane] + b->stat_l[ob][k][1][lane] + b->stat_l[ob][k][2][lane] + b->stat_l[ob][k][3][lane], L);
         }
-        const float inv = L == 0.0f ? 0.0f : (1.0f / kBase) / L;
+        const float inv = L == 0.0f ? 0.0f : b->stat_ref[ob] * (1.0f / kBase) / L;
 #pragma unroll
         for (int k = 0; k < S::kTurns; ++k) f[k] *= inv;
         if (wq == 0) {
