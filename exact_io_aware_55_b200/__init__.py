@@ -282,7 +282,7 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 
 def _launch(fn, device: int, stream, *args):
     """Calls fn(*args, stream) with GPU `device` current, on `stream` or that GPU's current stream."""
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         st = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
@@ -292,7 +292,7 @@ def _launch(fn, device: int, stream, *args):
 
 
 # A decode step makes these calls once per layer and token, so the checks are written for few Python steps.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _check_as(t, name, shape, dtypes, device):
@@ -313,7 +313,6 @@ def _dims(t):
     return t.shape
 
 
-_Strides = ctypes.c_longlong * 3
 _I32, _F32, _F64, _BF16 = (torch.int32,), (torch.float32,), (torch.float64,), (torch.bfloat16,)
 
 
@@ -334,35 +333,44 @@ def fa_rope(x, y, positions, inv_freq, factor: float = 1.0, interleaved: bool = 
             stream=None) -> None:
     """y <- x [B,H,N,d] bf16 with rotary positions on its first 2 * len(inv_freq) elements.  x and y may have any
     batch, head and token strides (d contiguous); y may be x.  positions: int32 [B,N], or None for 0..N-1."""
-    B, H, N, d = shape = _dims(x)
     dev = _gpu_index(x)
+    if y.shape != x.shape or y.dtype is not torch.bfloat16 or y.get_device() != dev or y.dim() != 4 or y.stride(3) != 1:
+        raise ValueError(f"y: expected bf16 {tuple(x.shape)} on cuda:{dev} with d contiguous, got {y.dtype} "
+                         f"{tuple(y.shape)} on {y.device}")
+    _rope(x, y, y.stride(), positions, inv_freq, factor, interleaved, transpose, stream, dev)
+
+
+def _rope(x, y, y_stride, positions, inv_freq, factor, interleaved, transpose, stream, dev):
+    B, H, N, d = _dims(x)
     xb, xh, xn, xd = x.stride()
-    yb, yh, yn, yd = y.stride() if y.dim() == 4 else (0, 0, 0, 0)
-    if x.dtype is not torch.bfloat16 or y.dtype is not torch.bfloat16 or y.shape != shape or y.get_device() != dev \
-            or xd != 1 or yd != 1:
-        raise ValueError(f"x and y must be bf16 of one shape on one GPU with d contiguous, got {x.dtype} {tuple(shape)} "
-                         f"on {x.device} and {y.dtype} {tuple(y.shape)} on {y.device}")
+    if x.dtype is not torch.bfloat16 or xd != 1:
+        raise ValueError(f"x: expected bf16 with d contiguous, got {x.dtype} with strides {x.stride()}")
     if positions is not None:
         _check_as(positions, "positions", (B, N), _I32, dev)
+        positions = positions.data_ptr()
     pairs = inv_freq.numel()
     _check_as(inv_freq, "inv_freq", (pairs,), _F64, dev)
-    _launch(lib.fa_rope, dev, stream, x.data_ptr(), y.data_ptr(), 0 if positions is None else positions.data_ptr(),
-            inv_freq.data_ptr(), factor, B, H, N, d, 2 * pairs, 1 if interleaved else 0, 1 if transpose else 0,
-            _Strides(xb, xh, xn), _Strides(yb, yh, yn))
+    _launch(lib.fa_rope, dev, stream, x.data_ptr(), y.data_ptr(), positions, inv_freq.data_ptr(), factor, B, H, N, d,
+            2 * pairs, 1 if interleaved else 0, 1 if transpose else 0, xb, xh, xn, y_stride[0], y_stride[1], y_stride[2])
+
+
+def _rope_new(x, positions, inv_freq, factor, interleaved, transpose, stream):
+    B, H, N, d = _dims(x)
+    dev = _gpu_index(x)
+    stride = (H * N * d, N * d, d, 1)
+    y = torch.empty_strided((B, H, N, d), stride, dtype=torch.bfloat16, device=x.device)
+    _rope(x, y, stride, positions, inv_freq, factor, interleaved, transpose, stream, dev)
+    return y
 
 
 def rope_forward(x, positions, inv_freq, interleaved: bool = False, factor: float = 1.0, stream=None):
     """Rotary positions on x, as a new contiguous tensor."""
-    y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    fa_rope(x, y, positions, inv_freq, factor, interleaved, False, stream)
-    return y
+    return _rope_new(x, positions, inv_freq, factor, interleaved, False, stream)
 
 
 def rope_backward(dy, positions, inv_freq, interleaved: bool = False, factor: float = 1.0, stream=None):
     """Gradient of rope_forward with respect to x, as a new contiguous tensor."""
-    dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
-    fa_rope(dy, dx, positions, inv_freq, factor, interleaved, True, stream)
-    return dx
+    return _rope_new(dy, positions, inv_freq, factor, interleaved, True, stream)
 
 
 def fa_page_tables(ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens,

@@ -79,7 +79,7 @@ def _load() -> ctypes.CDLL:
     dbl, ll = ctypes.c_double, ctypes.c_longlong
     lib.fa_rope_frequencies.argtypes = [ctypes.POINTER(dbl), ctypes.POINTER(dbl), i, dbl, i, dbl, dbl, dbl, dbl]
     lib.fa_rope_frequencies.restype = i
-    lib.fa_rope.argtypes = [vp, vp, vp, vp, f, i, i, i, i, i, i, i, ctypes.POINTER(ll), ctypes.POINTER(ll), vp]
+    lib.fa_rope.argtypes = [vp, vp, vp, vp, f, i, i, i, i, i, i, i, ll, ll, ll, ll, ll, ll, vp]
     lib.fa_rope.restype = i
     lib.fa_page_tables.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
     lib.fa_page_tables.restype = i

@@ -700,8 +700,8 @@ fa_status fa_rope_frequencies(double* inv_freq, double* attention_factor, int ro
 }
 
 fa_status fa_rope(const void* x, void* y, const int* positions, const double* inv_freq, float factor, int B, int H,
-                  int N, int d, int rot_dim, int interleaved, int transpose, const long long* x_strides,
-                  const long long* y_strides, void* stream) {
+                  int N, int d, int rot_dim, int interleaved, int transpose, long long xb, long long xh, long long xn,
+                  long long yb, long long yh, long long yn, void* stream) {
   if (B < 0 || H < 0 || N < 0) return FA_ERR_INVALID_ARG;
   if ((interleaved != 0 && interleaved != 1) || (transpose != 0 && transpose != 1)) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(factor)) return FA_ERR_INVALID_ARG;
@@ -709,8 +709,9 @@ fa_status fa_rope(const void* x, void* y, const int* positions, const double* in
   if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H > 65535 || static_cast<long long>(B) * N > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
   if (B == 0 || H == 0 || N == 0) return FA_OK;
-  if (!x || !y || !inv_freq || !x_strides || !y_strides) return FA_ERR_INVALID_ARG;
+  if (!x || !y || !inv_freq) return FA_ERR_INVALID_ARG;
   const int sizes[3] = {B, H, N};
+  const long long x_strides[3] = {xb, xh, xn}, y_strides[3] = {yb, yh, yn};
   for (int i = 0; i < 3; ++i) {
     if (x_strides[i] < 0 || y_strides[i] < 0) return FA_ERR_INVALID_ARG;
     if (sizes[i] > 1 && y_strides[i] < d) return FA_ERR_INVALID_ARG;      // rows of the output would overlap

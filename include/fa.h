@@ -334,11 +334,11 @@ FA_API fa_status fa_rope_frequencies(double* inv_freq, double* attention_factor,
  *   u' = factor * (u cos a - w sin a),  w' = factor * (w cos a + u sin a),
  * and copies the other d - rot_dim elements.  transpose != 0 turns by -a: the
  * gradient of the call with respect to x, applied to the gradient of y.
- *   x, y        : in/out, bf16 [B,H,N,d] with strides: x_strides and y_strides
- *                 (host arrays) give the elements from one batch, head and
- *                 token to the next; d is contiguous.  y may be x with equal
- *                 strides (in place); otherwise they must not overlap.  An
- *                 input may repeat rows (stride 0), an output may not.
+ *   x, y        : in/out, bf16 [B,H,N,d] with strides: xb, xh, xn and yb, yh, yn
+ *                 are the elements from one batch, head and token to the next;
+ *                 d is contiguous.  y may be x with equal strides (in place);
+ *                 otherwise they must not overlap.  An input may repeat rows
+ *                 (stride 0), an output may not.
  *   positions   : in, int32 [B,N] (any value), or NULL for 0..N-1
  *   inv_freq    : in, fp64 [rot_dim/2], device memory, 8-byte aligned
  *   interleaved : pairs are elements (2i, 2i+1), else (i, i + rot_dim/2)
@@ -346,8 +346,8 @@ FA_API fa_status fa_rope_frequencies(double* inv_freq, double* attention_factor,
  * Angles are reduced in 64 bits, so positions of 10^6 and more keep their accuracy.
  */
 FA_API fa_status fa_rope(const void* x, void* y, const int* positions, const double* inv_freq, float factor, int B,
-                         int H, int N, int d, int rot_dim, int interleaved, int transpose,
-                         const long long* x_strides, const long long* y_strides, void* stream);
+                         int H, int N, int d, int rot_dim, int interleaved, int transpose, long long xb,
+                         long long xh, long long xn, long long yb, long long yh, long long yn, void* stream);
 
 /*
  * Page tables of a batch, built on the GPU from request lengths.  Request b

@@ -13,19 +13,18 @@ F, C = ctypes.c_float, fa.STATUS_CODES
 P = 4096
 NO_GPU = (C["FA_ERR_ARCH"], C["FA_ERR_LAUNCH"])     # got past every argument check
 gpu = fa.lib.fa_get_device_status(None) != C["FA_ERR_ARCH"]
-LL3 = ctypes.c_longlong * 3
 
 
 def rope(x=P, y=2 * P, pos=P, freq=P, factor=1.0, B=1, H=2, N=8, d=64, rot=64, inter=0, tr=0, xs=(1024, 512, 64),
          ys=(1024, 512, 64)):
-    return fa.lib.fa_rope(x, y, pos, freq, F(factor), B, H, N, d, rot, inter, tr, xs and LL3(*xs), ys and LL3(*ys), None)
+    return fa.lib.fa_rope(x, y, pos, freq, F(factor), B, H, N, d, rot, inter, tr, *xs, *ys, None)
 
 
 def test_rope_argument_errors():
     assert rope(d=96) == C["FA_ERR_UNSUPPORTED"]
     assert rope(rot=8) == rope(rot=24) == rope(rot=128) == C["FA_ERR_UNSUPPORTED"]
     assert rope(B=-1) == rope(inter=2) == rope(tr=-1) == rope(factor=math.inf) == C["FA_ERR_INVALID_ARG"]
-    assert rope(x=None) == rope(y=None) == rope(freq=None) == rope(xs=None) == C["FA_ERR_INVALID_ARG"]
+    assert rope(x=None) == rope(y=None) == rope(freq=None) == C["FA_ERR_INVALID_ARG"]
     assert rope(xs=(-8, 512, 64)) == C["FA_ERR_INVALID_ARG"]
     assert rope(B=2, ys=(0, 512, 64)) == C["FA_ERR_INVALID_ARG"]          # output rows on one another
     assert rope(ys=(0, 512, 32)) == C["FA_ERR_INVALID_ARG"]
