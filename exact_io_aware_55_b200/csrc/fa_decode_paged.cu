@@ -1023,7 +1023,8 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       // left that piece is also why this one, which may have had no tile to wait
       // for in this piece, is not ahead of q_empty's phase.
       if (it >= 2) ok = ok && pg_wait(&b->o_free[ob], ((it >> 1) + 1) & 1, wc, WAIT_PAGED_O_FREE);
-      if (ok && group == 0 && wq == 0 && lane == 0) b->stat_ref[ob] = b->page_ref[qb];
+      // (by a group that had a tile, and with it waited for the piece's queries)
+      if (ok && began && part == 0 && wq == 0 && lane == 0) b->stat_ref[ob] = b->page_ref[qb];
       if (ok && lane == 0) mbar_arrive(&b->q_empty[qb]);
       if (ok && began) {
         const float l = rows_sum<H>(l_t, lane);      // of row lane / (32 / H)
