@@ -858,7 +858,7 @@ fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void
   a.num_pages = num_pages;
   a.page = page_size;
   a.max_pages = num_pages > 0 ? max_pages : 0;    // without pages every request is empty
-  a.causal = causal;
+  a.causal = causal && Nq > 1;                    // a single query sees every key either way
   a.c_log2 = scale * kLog2e;
   CUtensorMap tk{}, tv{};
   if (a.max_pages > 0 && (!make_map_pages(&tk, k_cache, d, page_size, num_pages * Hkv) ||

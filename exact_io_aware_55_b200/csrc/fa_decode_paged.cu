@@ -32,18 +32,20 @@
 // cut into tiles of 128 (d = 128) or 256 (d = 64) tokens, 32 KB of codes.  The
 // lengths are known on the device only, so every CTA adds them up itself and
 // takes an equal share of all tiles (a unit counts for two more), a contiguous
-// range that may begin and end inside a unit.  A unit that lies within one CTA is written directly; of a
-// unit cut between CTAs each CTA leaves its normalised O and LSE in one of its
+// range that may begin and end inside a unit.  A unit that lies within one CTA is
+// written directly; of a unit cut between CTAs each CTA leaves its normalised O and LSE in one of its
 // two slots of the workspace (one for a piece that does not begin its unit, one
 // for a piece that does), and the CTA that is the last to finish a piece of the
 // unit combines them by their log-sum-exp, in the order of the pieces, so that
 // results do not depend on timing.
 //
-// Warps: 0 page ids and TMA, 1 S products and TMEM owner, 2 page scales and
-// queries, 3 PV products, from 4 on the softmax groups of four (thread = key, each group its
-// share of the rows; TMEM lane quarter = warp % 4), the last four epilogue.  Pages that lie behind the length or outside the cache are not
-// loaded; the softmax warps clear the V rows of keys that are not there, since
-// p = 0 times a stale NaN code would be NaN.
+// Warps: 0 K and V pages, 1 S products and TMEM owner, 2 page scales, queries
+// and, with many small pages, V pages, 3 PV products; from 4 on the softmax
+// groups of four (thread = key, each group its share of the rows; TMEM lane
+// quarter = warp % 4), the last four epilogue.  Pages that lie behind the length
+// or outside the cache are not loaded; the softmax warps clear the V rows of keys
+// that are not there, since p = 0 times a stale NaN code would be NaN.
+//
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -59,7 +61,7 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 // What a piece costs beside its tiles, in tiles (measured: a batch of 256 x 512
-// keys takes 72 us with 0, XX with 2).
+// keys takes 72 us with 0, 65 with 2).
 constexpr int kPieceCost = 2;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
 constexpr float kBase = 2048.0f;            // P is scaled by 2^11: at most 2^15, of e5m2's 57344
@@ -86,7 +88,6 @@ struct PgShape {
   // columns at least), the low part 16 times itself; from 16 rows on both products
   // go into the same columns, the low part as it is, in e5m2, whose range it needs.
   static constexpr bool kFold = R >= 16;
-  static constexpr float kLoScale = 16.0f;                    // where it is not folded
   static constexpr int kQRows = 2 * R;                        // hi, lo
   static constexpr int kSCols = kFold ? R : 2 * R;
   static constexpr int kQBytes = kQRows * D;
@@ -207,49 +208,21 @@ __device__ __forceinline__ bool pg_wait3(uint64_t* x, uint32_t px, uint64_t* y, 
          (pg_wait_slow(x, px, w, where) && pg_wait_slow(y, py, w, where) && pg_wait_slow(z, pz, w, where));
 }
 
-// N (4, 8, 16) consecutive TMEM columns of this thread's lane.
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[N]) {
-  if constexpr (N == 4)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(t) : "memory");
-  else if constexpr (N == 8)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(t) : "memory");
-  else
-    tmem_ld_x16(t, r);
+// Eight consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t) : "memory");
 }
 // Two such loads with one wait.
-template <int N>
-__device__ __forceinline__ void tmem_ld2(uint32_t t, uint32_t t2, uint32_t (&r)[N], uint32_t (&q)[N]) {
-  if constexpr (N == 4)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%8];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%9];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-                 : "r"(t), "r"(t2) : "memory");
-  else if constexpr (N == 8)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7])
-                 : "r"(t), "r"(t2) : "memory");
-  else {
-    tmem_ld_x16(t, r);
-    tmem_ld_x16(t2, q);
-  }
-}
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[N]) {
-  if constexpr (N == 4)
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]) : "memory");
-  else if constexpr (N == 8)
-    tmem_st_x8(t, r);
-  else
-    tmem_st_x16(t, r);
+__device__ __forceinline__ void tmem_ld2(uint32_t t, uint32_t t2, uint32_t (&r)[8], uint32_t (&q)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+               "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7])
+               : "r"(t), "r"(t2) : "memory");
 }
 // Sums over the warp of H = 8 values per lane; lane gets that of value
 // lane / 4.  Each step but the last two halves the values: a lane keeps one half
@@ -433,6 +406,23 @@ struct PageBatch {
     w.left -= tiles;
     return row;
   }
+  // Loads the pages of tile `tile` of the batch, whose rows the lanes hold, of one
+  // map or of two (the second `apart` bytes behind), and arrives at `bar` with
+  // their bytes.  A copy per lane, 67 cycles for each (issued in a loop by the
+  // converged warp it took twice that).
+  __device__ __forceinline__ void load(const CUtensorMap& map, const CUtensorMap* map2, int apart, int row, int tile,
+                                       uint8_t* dst, int d, uint64_t* bar, uint64_t pol) const {
+    const int page_bytes = w.a.page * d;
+    const uint32_t in_tile = per_tile == 32 ? 0xffffffffu : ((1u << per_tile) - 1u) << (tile * per_tile);
+    const int bytes = page_bytes * __popc(__ballot_sync(0xffffffffu, row >= 0) & in_tile);
+    mbar_arrive_expect_tx_e(bar, map2 ? 2 * bytes : bytes);
+    __syncwarp();
+    if (u == tile && row >= 0) {
+      tma_load_3d_hint(dst + i * page_bytes, &map, bar, 0, 0, row, pol);
+      if (map2) tma_load_3d_hint(dst + apart + i * page_bytes, map2, bar, 0, 0, row, pol);
+    }
+    __syncwarp();
+  }
 };
 
 // Marks this CTA's piece of a unit as done and looks whether all of them are,
@@ -543,7 +533,9 @@ __device__ __forceinline__ void merge_unit(const PagedArgs& a, const Merge& u, u
   }
 }
 
-template <int D, int R>
+// CAUSAL: a boundary between keys that some queries see and others do not.
+// SHARED: K and V pages are loaded by a warp each.
+template <int D, int R, bool CAUSAL, bool SHARED>
 __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const PagedArgs a) {
@@ -587,7 +579,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       b->abort = 0u;
     }
     fence_mbar_init();
-  } else if (warp >= S::kEpi) {
+  } else if (CAUSAL && warp >= S::kEpi) {
     for (int i = threadIdx.x - 32 * S::kEpi; i < 256; i += 128) b->nan_keys[i >> 7][i & 127] = 0u;
   }
   if (R == 8 && warp >= 4 && warp < 8) {             // the zero rows of P^T
@@ -658,14 +650,14 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
   const Place start = b->start;
   const int per = b->per, n_tiles = static_cast<int>(b->first_tile[1] - b->first_tile[0]);
 
+  // the cache is streamed once, unless several row tiles read it
+  const uint64_t pol = a.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
   if (n_tiles == 0) {
     // nothing but the empty requests below
   } else if (warp == 0) {
-    // ------------------------------------------------------------ producer
+    // ------------------------------------------- K pages, V pages if few
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    // the cache is streamed once, unless several row tiles read it
-    const uint64_t pol = a.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
     PageBatch<TILE> pb(a, start, n_tiles, lane);
     int row = pb.fetch();
     bool ok = true;
@@ -673,22 +665,13 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       const int next = pb.fetch();
       const int m = min(pb.tiles, n_tiles - t0);
       if (row == -2) report_status(a.status, DEVSTATUS_BAD_PAGE, WAIT_PAGED_TABLE);
-      const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
       for (int u = 0; u < m; ++u) {
         const int t = t0 + u, s = t % NS;
         if (t >= NS && !pg_wait(&b->kv_empty[s], ((t / NS) + 1) & 1, wc, WAIT_PAGED_KV_EMPTY)) {
           ok = false;
           break;
         }
-        const uint32_t in_tile = pb.per_tile == 32 ? 0xffffffffu : ((1u << pb.per_tile) - 1u) << (u * pb.per_tile);
-        mbar_arrive_expect_tx_e(&b->kv_full[s], 2u * D * a.page * __popc(have & in_tile));
-        __syncwarp();
-        if (pb.u == u && row >= 0) {
-          uint8_t* st = sKV + s * S::kStageBytes + pb.i * a.page * D;
-          tma_load_3d_hint(st, &tmK, &b->kv_full[s], 0, 0, row, pol);
-          tma_load_3d_hint(st + S::kTileBytes, &tmV, &b->kv_full[s], 0, 0, row, pol);
-        }
-        __syncwarp();
+        pb.load(tmK, SHARED ? nullptr : &tmV, S::kTileBytes, row, u, sKV + s * S::kStageBytes, D, &b->kv_full[s], pol);
       }
       row = next;
     }
@@ -759,7 +742,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       if (j + 1 == n) tc_commit_e(&b->o_full[ob]);
     }
   } else if (warp == 2) {
-    // --------------------------------------------- page scales and queries
+    // ---------------------------- V pages if many, page scales and queries
     PageBatch<TILE> pb(a, start, n_tiles, lane);
     int row = pb.fetch();
     float ks = row >= 0 ? a.k_scale[row] : 0.0f, vs = row >= 0 ? a.v_scale[row] : 0.0f;
@@ -813,7 +796,10 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           b->page[s][pb.i] = row >= 0 ? make_float4(ks * a.c_log2, lv - ref, iv * ref2, vs)
                                       : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->kv_full[s]);
+        if (SHARED)
+          pb.load(tmV, nullptr, 0, row, u, sKV + s * S::kStageBytes + S::kTileBytes, D, &b->kv_full[s], pol);
+        else if (lane == 0)
+          mbar_arrive(&b->kv_full[s]);
       }
       row = next;
       ks = row >= 0 ? a.k_scale[row] : 0.0f;
@@ -858,13 +844,13 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           const uint32_t col = lane_base + S::kColS + S::kSCols * (sb * U + u) + hr;
           uint32_t x[H], y[H];
           if constexpr (S::kFold) {
-            tmem_ld<H>(col, x);
+            tmem_ld(col, x);
 #pragma unroll
             for (int r = 0; r < H; ++r) s[u][r] = __uint_as_float(x[r]);
           } else {
-            tmem_ld2<H>(col, col + R, x, y);
+            tmem_ld2(col, col + R, x, y);
 #pragma unroll
-            for (int r = 0; r < H; ++r) s[u][r] = fmaf(__uint_as_float(y[r]), 1.0f / S::kLoScale, __uint_as_float(x[r]));
+            for (int r = 0; r < H; ++r) s[u][r] = fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r]));
           }
         }
         tc_fence_before();
@@ -894,7 +880,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             for (int c = 0; c < D / S::kSplit / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        if (a.causal && tile0 + TILE > pc.len - a.Nq + 1) {
+        if (CAUSAL && tile0 + TILE > pc.len - a.Nq + 1) {
           // V codes that are NaN must not meet p = 0 either: of a key that not
           // every query sees they are cleared here, and noted for the epilogue
 #pragma unroll
@@ -968,10 +954,10 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
               for (int k = 0; k < 3; ++k) {
                 const uint32_t col = lane_base + S::kColO + S::kPRows * (S::kTurns * ob + turn) + k * R + hr;
                 uint32_t o[H];
-                tmem_ld<H>(col, o);
+                tmem_ld(col, o);
 #pragma unroll
                 for (int r = 0; r < H; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
-                tmem_st<H>(col, o);
+                tmem_st_x8(col, o);
               }
               tmem_wait_st();
             }
@@ -1089,7 +1075,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       }
       ok = ok && pg_wait(&b->o_full[ob], (it >> 1) & 1, wc, WAIT_PAGED_O);
       tc_fence_after();
-      const uint32_t bad = drow >= 0 ? b->nan_keys[ob][drow] : 0u;
+      const uint32_t bad = CAUSAL && drow >= 0 ? b->nan_keys[ob][drow] : 0u;
       constexpr int kStep = R == 8 ? 8 : 16;
 #pragma unroll 1
       for (int rg = 0; rg < R; rg += kStep) {
@@ -1124,7 +1110,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
             o[k] = t == 0 ? y : o[k] + y;
           }
         }
-        if (bad != 0u) {     // query i sees the boundary keys 0..i-1
+        if (CAUSAL && bad != 0u) {     // query i sees the boundary keys 0..i-1
           int i = (row0 + rg) % a.Nq;
 #pragma unroll
           for (int k = 0; k < kStep; ++k) {
@@ -1146,7 +1132,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           }
         }
       }
-      if (bad != 0u) b->nan_keys[ob][drow] = 0u;
+      if (CAUSAL && bad != 0u) b->nan_keys[ob][drow] = 0u;
       tc_fence_before();
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&b->o_free[ob]);
@@ -1184,11 +1170,11 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
   for (int i = 0; i < n_merge; ++i) merge_unit<D, R>(a, b->merge[i], smem, &b->merged, phase, wc);
 }
 
-template <int D, int R>
-cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t stream) {
+template <int D, int R, bool CAUSAL, bool SHARED>
+cudaError_t launch_paged_v(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t stream) {
   constexpr size_t smem = pg_smem_bytes<D, R>();
   static_assert(smem <= 227 * 1024, "shared memory budget");
-  auto kern = decode_paged_kernel<D, R>;
+  auto kern = decode_paged_kernel<D, R, CAUSAL, SHARED>;
   static std::atomic<unsigned long long> configured{0};       // a bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1199,6 +1185,22 @@ cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const P
     if (dev <= 63) configured.fetch_or(1ull << dev, std::memory_order_release);
   }
   return launch_dependent(kern, dim3(kPagedCtas), dim3(PgShape<D, R>::kThreads), smem, stream, tk, tv, a);
+}
+
+template <int D, int R>
+cudaError_t launch_paged_t(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t stream) {
+  // With more than four pages a tile the copies of K and V together take one warp
+  // longer than the tile, so each has a warp of its own (B32 n8192, pages of 16:
+  // 60.4 us with one warp, 57.7 with two; pages of 64: 54.3 and 55.5, the second
+  // warp has the scales and queries to do). With few tiles a CTA that second
+  // warp's start counts for more (B1 n1000: 12.4 and 13.6 us; B7 n5003, eight
+  // tiles a CTA: 22.5 and 23.6). How many there are is known here by what the
+  // table can hold.
+  constexpr int kTile = PgShape<D, R>::kTileKeys;
+  const int64_t tiles = int64_t(a.B) * a.Hkv * ((int64_t(a.max_pages) * a.page + kTile - 1) / kTile);
+  const bool shared = kTile / a.page > 4 && tiles > 16 * kPagedCtas;
+  if (a.causal) return shared ? launch_paged_v<D, R, true, true>(tk, tv, a, stream) : launch_paged_v<D, R, true, false>(tk, tv, a, stream);
+  return shared ? launch_paged_v<D, R, false, true>(tk, tv, a, stream) : launch_paged_v<D, R, false, false>(tk, tv, a, stream);
 }
 
 }  // namespace

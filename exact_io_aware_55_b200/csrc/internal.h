@@ -65,7 +65,6 @@ enum WaitSite : uint32_t {
   WAIT_PAGED_KV_EMPTY = 73,
   WAIT_PAGED_SC_EMPTY = 74,
   WAIT_PAGED_S = 75,
-  WAIT_PAGED_S_FREE = 76,
   WAIT_PAGED_P = 77,
   WAIT_PAGED_PV = 78,
   WAIT_PAGED_MERGE = 79,
