@@ -96,7 +96,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
       if (*w.abort_flag) return false;
       if (globaltimer_ns() - t0 > w.limit_ns) {
         *w.abort_flag = 1u;
-        if (atomicCAS(&w.status[0], DEVSTATUS_OK, DEVSTATUS_WAIT_TIMEOUT) == DEVSTATUS_OK)
+        // in place of a skipped page too, after which outputs are still defined
+        if (atomicExch(&w.status[0], DEVSTATUS_WAIT_TIMEOUT) != DEVSTATUS_WAIT_TIMEOUT)
           atomicExch(&w.status[1], where);
         return false;
       }

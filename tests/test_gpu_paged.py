@@ -427,6 +427,15 @@ def test_decode_lengths_outside_the_table():
     check_decode(*case, 0.125, False, 64)
 
 
+def test_a_timeout_is_reported_over_a_skipped_page():
+    k = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    cache, scales = torch.zeros(3, 1, 16, 64, dtype=torch.uint8, device="cuda"), torch.ones(3, 1, device="cuda")
+    slots = torch.tensor([[3 * 16, 1, 2, 3]], dtype=torch.int32, device="cuda")
+    fa.fa_cache_append_fp8(k, k, slots, cache, cache.clone(), scales, scales.clone())
+    fa.fa_watchdog_selftest(2000)
+    assert fa.fa_device_status() == (fa.STATUS_CODES["FA_ERR_DEVICE_TIMEOUT"], 99)
+
+
 def test_decode_repeat_is_identical():
     q, kc, vc, ks, vs, table, lens = decode_case(7, 16, 2, 2, 128, 16, [3000, 5, 800, 0, 129, 4000, 64], seed=84)
     args = (q[1], kc[1], vc[1], ks[1], vs[1], i32(table), i32(lens))
