@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <atomic>
 #include <chrono>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -714,9 +715,18 @@ fa_status fa_rope(const void* x, void* y, const int* positions, const double* in
   const long long x_strides[3] = {xb, xh, xn}, y_strides[3] = {yb, yh, yn};
   for (int i = 0; i < 3; ++i) {
     if (x_strides[i] < 0 || y_strides[i] < 0) return FA_ERR_INVALID_ARG;
-    if (sizes[i] > 1 && y_strides[i] < d) return FA_ERR_INVALID_ARG;      // rows of the output would overlap
     if (x == y && sizes[i] > 1 && x_strides[i] != y_strides[i]) return FA_ERR_INVALID_ARG;
     if (sizes[i] > 1 && (x_strides[i] % 8 != 0 || y_strides[i] % 8 != 0)) return FA_ERR_ALIGNMENT;
+  }
+  // rows of the output must not lie on one another: in order of the strides, each
+  // dimension steps over all that the ones before it cover
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int i, int j) { return y_strides[i] < y_strides[j]; });
+  long long covered = d;
+  for (int i : order) {
+    if (sizes[i] == 1) continue;
+    if (y_strides[i] < covered || y_strides[i] > LLONG_MAX / 4 / sizes[i]) return FA_ERR_INVALID_ARG;
+    covered += y_strides[i] * (sizes[i] - 1);
   }
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(inv_freq, 8) || !aligned(positions, 4)) return FA_ERR_ALIGNMENT;
   uint32_t* status = nullptr;

@@ -35,6 +35,16 @@ def test_rope_argument_errors():
     assert rope(N=0, x=None) == C["FA_OK"]
 
 
+def test_rope_refuses_output_rows_on_one_another():
+    bad = C["FA_ERR_INVALID_ARG"]
+    assert rope(B=2, H=2, N=8, ys=(512, 512, 64)) == bad                  # two batches in the same place
+    assert rope(B=1, H=2, N=8, ys=(0, 448, 64)) == bad                    # a head on the last token of the one before
+    assert rope(B=1, H=2, N=8, ys=(0, 64, 64)) == bad
+    assert rope(B=3, H=2, N=8, ys=(960, 512, 64)) == bad
+    assert rope(B=2, H=2, N=8, ys=(1 << 62, 512, 64)) == bad              # extents beyond 64 bits
+    assert rope(y=P, xs=(512, 512, 64), B=2, ys=(512, 512, 64)) == bad    # in place on repeated rows
+
+
 @pytest.mark.skipif(gpu, reason="the pointers are not memory")
 def test_valid_calls_reach_the_device_check():
     assert rope(pos=None, xs=(0, 0, 0)) in NO_GPU                         # repeated input rows are fine
