@@ -835,8 +835,12 @@ fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void
   if ((max_pages > 0 && !block_table) || (num_pages > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)))
     return FA_ERR_INVALID_ARG;
   const PagedPlan plan = paged_plan(H, Hkv, Nq, d);
-  // the tiles of one request, and one head's tiles of all, are counted in 32 bits
-  if (static_cast<long long>(B) * max_pages > 0x7fffffffll || (static_cast<long long>(max_pages) * page_size / 128 + 1) * Hkv * plan.row_tiles > 0x7fffffffll)
+  // table entries, a request's tiles and a CTA's share of all (a unit counts for
+  // two more) are counted in 32 bits
+  const long long units = static_cast<long long>(Hkv) * plan.row_tiles;
+  const long long tiles = (static_cast<long long>(max_pages) * page_size / 128 + 3) * units;
+  if (static_cast<long long>(B) * max_pages > 0x7fffffffll || tiles > 0x7fffffffll ||
+      tiles * B / fa::kPagedCtas > 0x70000000ll)
     return FA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < plan.total) return FA_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||

@@ -104,6 +104,12 @@ def test_decode_argument_errors():
         fa.fa_fwd_decode_paged_fp8_workspace_size(1, 7, 2, 1, 64)
 
 
+def test_decode_refuses_more_tiles_than_a_share_counts():
+    big = dict(H=256, hkv=256, Nq=1, page=128, mp=(1 << 22) + (1 << 20), d=128, pages=9)
+    assert decode(B=255, **big) == C["FA_ERR_UNSUPPORTED"]      # 1.25 * 2^22 * 256 * 255 / 148 > 2^31
+    assert decode(B=100, **big) == C["FA_ERR_WORKSPACE"]        # counted; the next check is the workspace's
+
+
 def test_python_wrappers_refuse():
     t = torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16)
     f = torch.zeros(8, dtype=torch.float64)
