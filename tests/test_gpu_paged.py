@@ -322,6 +322,46 @@ def test_decode_parity(B, H, Hkv, Nq, page, lens, d, causal):
     check_decode(*case, d ** -0.5, causal, d)
 
 
+WIDE = [  # B, H, Hkv, Nq, page, lens: tables that could hold far more than the requests have
+    (3, 8, 2, 1, 16, [900, 0, 5000]), (2, 32, 2, 1, 16, [4000, 17]), (2, 16, 2, 3, 16, [2100, 1300]), (1, 4, 2, 1, 32, [3001])]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hkv,Nq,page,lens", WIDE)
+def test_decode_wide_tables(B, H, Hkv, Nq, page, lens, d, causal):
+    q, kc, vc, ks, vs, table, n = decode_case(B, H, Hkv, Nq, d, page, lens, seed=B + H + d)
+    wide = np.full((B, 400_000 // (B * Hkv)), -1)
+    wide[:, : table.shape[1]] = table
+    a = check_decode(q, kc, vc, ks, vs, wide, n, d ** -0.5, causal, d)
+    b = check_decode(q, kc, vc, ks, vs, table, n, d ** -0.5, causal, d)
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_requests_that_share_pages(d):
+    """A common prompt: the first pages of every request are the same ones."""
+    q, kc, vc, ks, vs, table, n = decode_case(6, 8, 2, 2, d, 32, [700, 640, 641, 33, 699, 700], seed=88, stale=False)
+    table[:, :20] = table[0, :20]
+    check_decode(q, kc, vc, ks, vs, table, n, d ** -0.5, True, d)
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_decode_drawn_shapes_in_one_workspace(seed):
+    """Shapes drawn at random, one after the other in a workspace that the calls before have left as it is."""
+    rng = np.random.default_rng(100 + seed)
+    work = torch.empty(1 << 25, dtype=torch.uint8, device="cuda").random_()
+    for _ in range(4):
+        d, page = int(rng.choice([64, 128])), int(rng.choice([16, 32, 64, 128]))
+        Hkv, group, Nq, B = int(rng.integers(1, 6)), int(rng.choice([1, 2, 3, 4, 7, 8, 12])), int(rng.integers(1, 17)), int(rng.integers(1, 9))
+        lens = [int(2 ** rng.uniform(0, 12)) if rng.random() < 0.9 else 0 for _ in range(B)]
+        q, kc, vc, ks, vs, table, n = decode_case(B, group * Hkv, Hkv, Nq, d, page, lens, seed=int(rng.integers(2 ** 31)))
+        causal = bool(rng.integers(2))
+        o, lse = fa.attention_decode_paged_fp8(q[1], kc[1], vc[1], ks[1], vs[1], i32(table), i32(n), d ** -0.5, causal, work)
+        want = check_decode(q, kc, vc, ks, vs, table, n, d ** -0.5, causal, d)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("mult", [8.0, 64.0, 2.0 ** -40, 2.0 ** 30])
 def test_decode_score_ranges(mult, d):
