@@ -1,6 +1,6 @@
 // The 8-bit paged KV cache: writing new tokens into it, and its page tables.
 //
-// cache_append_kernel.  A page holds kPage tokens of one KV head as e4m3 codes
+// cache_append_kernel.  A page holds PAGE tokens of one KV head as e4m3 codes
 // with one scale, value = code * scale.  The tokens that a call writes to one
 // page are quantised together:
 //   e      = smallest exponent with amax <= 448 * 2^e over the finite new values
@@ -11,17 +11,19 @@
 // Scales are powers of two: a floating code gains nothing from a finer one,
 // x / scale' is exact, and so is moving old codes to a larger scale except
 // where they fall among the type's subnormals.  A page is written by one group
-// of threads that holds all of it, 64 elements per thread, in registers: the
-// new values are read once.
+// of threads that holds all of it, 64 elements per thread (fewer where a page is
+// small), in registers: the new values are read once.  Many tokens are bound by
+// memory, 3 bytes per element (B4 Hkv8 N8192 d128, 164 MB: 32-35 us, 4.6-5.1
+// TB/s), a few by a chain of loads, slot, scale, values (B64 N1: 4.2 us, most
+// of it the launch).
 //
 // page_tables_kernel.  See the comment there.
-//
-// Both are bound by memory or, for a few tokens, by the latency of a chain of
-// dependent loads.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -259,7 +261,7 @@ cudaError_t launch_append_t(AppendArgs a, cudaStream_t stream) {
 // every read of an input before the write of an output that may be the same
 // memory.
 constexpr int kTabThreads = 1024;
-constexpr int kTabCluster = 8;
+constexpr int kTabCluster = 16;       // B24 N8192: 12.9 us, with 8 (the portable size) 15.1; B1024 N1: 8.3 and 8.5
 
 struct TabRow {
   int ctx, nw, held, start, need;      // nw < 0: no slots
@@ -332,21 +334,36 @@ __global__ void __launch_bounds__(kTabThreads) __cluster_dims__(kTabCluster, 1, 
   if (!fits && warp == 0 && lane == 0) report_status(a.status, DEVSTATUS_BAD_PAGE, WAIT_TABLES_BACK);
   const int low = fits ? head - static_cast<int>(carry) : head;   // else the lists contradict each other: nothing comes back
   if (fits && carry > 0) {
-    int start = 0;
+    unsigned start = 0;
     for (int base = 0; base < a.B; base += kTabThreads) {
       if (!once) {
         load(base + threadIdx.x, back);
         end = block_scan(static_cast<unsigned long long>(back) << 32, s_warp, total);
       }
-      s_row[threadIdx.x] = TabRow{0, 0, back, start + static_cast<int>(end >> 32) - back, 0};
-      start += static_cast<int>(total >> 32);
+      s_row[threadIdx.x] = TabRow{0, 0, back, static_cast<int>(start + static_cast<unsigned>(end >> 32)) - back, 0};
+      const unsigned end_of_batch = start + static_cast<unsigned>(total >> 32);
       __syncthreads();
+      // page i of all is the last row's whose pages begin at or before it; four
+      // at a time, so that their loads are on their way together
       const int rows = min(kTabThreads, a.B - base);
+      constexpr int kAll = kTabCluster * kTabThreads;
 #pragma unroll 1
-      for (int r = warp; r < rows; r += kWarps)
-#pragma unroll 4
-        for (int i = lane; i < s_row[r].held; i += 32)
-          a.free_pages[low + s_row[r].start + i] = a.block_table[static_cast<long long>(base + r) * a.max_pages + i];
+      for (unsigned i0 = start + rank * kTabThreads + threadIdx.x; i0 < end_of_batch; i0 += 4 * kAll) {
+        int page[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned i = i0 + k * kAll;
+          int r = 0;
+#pragma unroll
+          for (int step = kTabThreads / 2; step > 0; step >>= 1)
+            if (r + step < rows && static_cast<unsigned>(s_row[r + step].start) <= i) r += step;
+          page[k] = i < end_of_batch ? a.block_table[static_cast<long long>(base + r) * a.max_pages + (i - s_row[r].start)] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i0 + k * kAll < end_of_batch) a.free_pages[low + (i0 + k * kAll)] = page[k];
+      }
+      start = end_of_batch;
       __syncthreads();
     }
   }
@@ -378,34 +395,38 @@ __global__ void __launch_bounds__(kTabThreads) __cluster_dims__(kTabCluster, 1, 
     if (asked <= avail && threadIdx.x == 0) s_taken = static_cast<int>(asked);
     __syncthreads();
     const int rows = min(kTabThreads, a.B - base);
-    // Slot of new token t; the first one on a new page enters it in the table.
-    auto slot = [&](const TabRow& w, int r, int t, int& pos) {
-      pos = 0;
+    // Page of new token t (-1: none), and its slot; the first token on a new page
+    // enters it in the table.  Apart, so that the loads of several tokens are on
+    // their way together.
+    auto page_of = [&](const TabRow& w, int r, int t) {
       if (t >= w.nw) return -1;
-      pos = w.ctx + t;
-      const int lp = pos >> shift;
-      int* entry = a.block_table + static_cast<long long>(base + r) * a.max_pages + lp;
-      const int page = lp < w.held ? *entry : a.free_pages[w.start + lp - w.held];
-      if (lp >= w.held && (pos & (P - 1)) == 0) *entry = page;
-      return page >= 0 && page < 0x7fffffff / P ? (page << shift) + (pos & (P - 1)) : -1;
+      const int lp = (w.ctx + t) >> shift;
+      return lp < w.held ? a.block_table[static_cast<long long>(base + r) * a.max_pages + lp] : a.free_pages[w.start + lp - w.held];
     };
-    if (a.N >= 32) {           // a warp takes 128 tokens of a request
-      const unsigned parts = (static_cast<unsigned>(a.N) + 127) >> 7;
+    auto put = [&](const TabRow& w, int r, int t, int page, long long at) {
+      const bool there = t < w.nw;
+      const int pos = there ? w.ctx + t : 0, lp = pos >> shift;
+      if (there && lp >= w.held && (pos & (P - 1)) == 0) a.block_table[static_cast<long long>(base + r) * a.max_pages + lp] = page;
+      a.slots[at] = there && page >= 0 && page < 0x7fffffff / P ? (page << shift) + (pos & (P - 1)) : -1;
+      a.positions[at] = pos;
+    };
+    if (a.N >= 32) {           // a warp takes 32 * kPer tokens of a request
+      constexpr int kPer = 8;
+      const unsigned parts = (static_cast<unsigned>(a.N) + 32 * kPer - 1) / (32 * kPer);
       const unsigned long long items = static_cast<unsigned long long>(parts) * rows;
       unsigned r = warp / parts, part = warp - r * parts;
 #pragma unroll 1
       for (unsigned long long i = warp; i < items; i += kWarps) {
         const TabRow w = s_row[r];
         const long long at = static_cast<long long>(base + r) * a.N;
+        const unsigned t0 = part * (32 * kPer) + lane;
+        int page[kPer];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int t = static_cast<int>(part * 128 + k * 32) + lane;
-          if (t < a.N) {
-            int pos;
-            a.slots[at + t] = slot(w, r, t, pos);
-            a.positions[at + t] = pos;
-          }
-        }
+        for (int k = 0; k < kPer; ++k)
+          page[k] = t0 + 32 * k < static_cast<unsigned>(a.N) ? page_of(w, r, static_cast<int>(t0 + 32 * k)) : -1;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (t0 + 32 * k < static_cast<unsigned>(a.N)) put(w, r, static_cast<int>(t0 + 32 * k), page[k], at + t0 + 32 * k);
         part += kWarps;
         const unsigned over = part / parts;
         r += over;
@@ -415,11 +436,8 @@ __global__ void __launch_bounds__(kTabThreads) __cluster_dims__(kTabCluster, 1, 
       const unsigned cells = static_cast<unsigned>(rows) * a.N;
 #pragma unroll 1
       for (unsigned i = rank * kTabThreads + threadIdx.x; i < cells; i += kTabCluster * kTabThreads) {
-        const unsigned r = i / static_cast<unsigned>(a.N);
-        int pos;
-        const long long at = static_cast<long long>(base) * a.N + i;
-        a.slots[at] = slot(s_row[r], r, i - r * a.N, pos);
-        a.positions[at] = pos;
+        const unsigned r = i / static_cast<unsigned>(a.N), t = i - r * a.N;
+        put(s_row[r], r, t, page_of(s_row[r], r, t), static_cast<long long>(base) * a.N + i);
       }
     }
     __syncthreads();
@@ -447,6 +465,15 @@ cudaError_t launch_cache_append(const AppendArgs& a, int d, cudaStream_t stream)
 }
 
 cudaError_t launch_page_tables(const TableArgs& a, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};       // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev > 63 || !((configured.load(std::memory_order_acquire) >> dev) & 1u)) {
+    e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) configured.fetch_or(1ull << dev, std::memory_order_release);
+  }
   return launch_dependent(page_tables_kernel, dim3(kTabCluster), dim3(kTabThreads), 0, stream, a);
 }
 
