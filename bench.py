@@ -392,8 +392,11 @@ def run_case(args):
     """One named path on --shape, for profiling (a short JSON line, not the
     bench line): 'decode' (B,H,Nk,d with --nq queries, causal), 'standard'
     (B,H,N,d: the materialising baseline, then the fused forward, per step),
-    'fp8' (B,H,N,d: the e4m3 forward) or 'det' (B,H,N,d: the backward with the
-    deterministic dQ pass, after one forward)."""
+    'fp8' (B,H,N,d: the e4m3 forward), 'det' (B,H,N,d: the backward with the
+    deterministic dQ pass, after one forward) or 'serve' (B,H,N,d: a decode step
+    of --nq tokens a request over an 8-bit paged cache of N/2 to N tokens, four
+    query heads to a KV head: page tables, rotary positions, the cache write and
+    the attention, captured into a CUDA graph; lengths grow from step to step)."""
     import torch
 
     import exact_io_aware_55_b200 as fa
@@ -439,6 +442,8 @@ def run_case(args):
         def step():
             fa.fa_fwd_fp8(q8, k8, v8, 0.01, 0.01, 0.01, o, lse, d ** -0.5, args.causal, stream)
         flops = fwd_flops(B, H, N, d, args.causal)
+    elif args.case == "serve":
+        step, nbytes = serve_step(args, B, H, N, d, dev, rnd)
     else:
         q, k, v = rnd(B, H, N, d), rnd(B, H, N, d), rnd(B, H, N, d)
         o = torch.empty_like(q)
@@ -468,6 +473,57 @@ def run_case(args):
     if flops:
         line["tflops"] = round(flops / ms / 1e9, 1)
     print(json.dumps(line), flush=True)
+
+
+def serve_step(args, B, H, N, d, dev, rnd):
+    """The captured decode step of --case serve, and the bytes of codes that its attention reads at first."""
+    import torch
+
+    import exact_io_aware_55_b200 as fa
+
+    nq, page = args.nq, 16
+    if H % 4 != 0:
+        raise SystemExit("--case serve needs a multiple of 4 heads")
+    Hkv = H // 4
+    grown = (args.steps + args.warmup + 1) * nq
+    per_row = -(-(N + grown) // page)
+    pages = B * per_row
+    i32 = {"dtype": torch.int32, "device": dev}
+    ctx = torch.linspace(N // 2, N, B, device=dev).to(torch.int32)
+    tokens = int(ctx.sum())
+    free = torch.randperm(pages, device=dev).to(torch.int32)
+    table = torch.full((B, per_row), -1, **i32)
+    head = torch.zeros(1, **i32)
+    slots, pos = torch.empty((B, nq), **i32), torch.empty((B, nq), **i32)
+    # the cache holds the prompts already: their pages are taken, their codes drawn
+    k_cache, v_cache = (torch.randint(0, 0x70, (pages, Hkv, page, d), dtype=torch.uint8, device=dev) for _ in range(2))
+    k_scale, v_scale = (torch.full((pages, Hkv), 2.0 ** -6, device=dev) for _ in range(2))
+    counts = [(-(-n // page)) for n in ctx.tolist()]
+    used = 0
+    for b, n in enumerate(counts):
+        table[b, :n] = free[used:used + n]
+        used += n
+    head.fill_(used)
+    new = torch.full((B,), nq, **i32)
+    q, k, v = rnd(B, H, nq, d), rnd(B, Hkv, nq, d), rnd(B, Hkv, nq, d)
+    qr, kr, o = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q)
+    lse = torch.empty((B, H, nq), device=dev)
+    freq, factor = fa.rope_frequencies(d, device=dev)
+    work = torch.empty(fa.fa_fwd_decode_paged_fp8_workspace_size(B, H, Hkv, nq, d), dtype=torch.uint8, device=dev)
+
+    def eager():
+        fa.fa_page_tables(ctx, new, free, head, table, slots, pos, ctx, head, page)
+        fa.fa_rope(q, qr, pos, freq, factor)
+        fa.fa_rope(k, kr, pos, freq, factor)
+        fa.fa_cache_append_fp8(kr, v, slots, k_cache, v_cache, k_scale, v_scale)
+        fa.fa_fwd_decode_paged_fp8(qr, k_cache, v_cache, k_scale, v_scale, table, ctx, o, lse, d ** -0.5, True, work)
+
+    eager()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        eager()
+    return graph.replay, 2 * tokens * Hkv * d
 
 
 def kernel_source_digest(files) -> str:
@@ -712,9 +768,9 @@ def main():
     ap.add_argument("--shape", default="", help="B,H,N,d of another workload (default: the bench workload)")
     ap.add_argument("--causal", action="store_true")
     ap.add_argument("--noncausal", action="store_true")
-    ap.add_argument("--case", choices=["decode", "standard", "fp8", "det"], default="",
+    ap.add_argument("--case", choices=["decode", "standard", "fp8", "det", "serve"], default="",
                     help="profile one path on --shape instead of the bench step")
-    ap.add_argument("--nq", type=int, default=1, help="queries per head for --case decode")
+    ap.add_argument("--nq", type=int, default=1, help="queries per head for --case decode and serve")
     ap.add_argument("--clock-window", type=float, default=1.5,
                     help="seconds of steps run under the clock sampler before the timed region")
     args = ap.parse_args()

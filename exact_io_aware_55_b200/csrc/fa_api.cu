@@ -893,7 +893,7 @@ const char* fa_strerror(fa_status s) {
     case FA_ERR_ARCH: return "current CUDA device is not an sm_100 (B200-class) GPU";
     case FA_ERR_LAUNCH: return "CUDA launch or tensor-map setup failed";
     case FA_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait ran out";
-    case FA_ERR_WORKSPACE: return "backward workspace missing or smaller than fa_bwd_workspace_size()";
+    case FA_ERR_WORKSPACE: return "workspace missing or smaller than the call's ..._workspace_size()";
     case FA_ERR_SCRATCH_LIMIT:
       return "shape needs more backward scratch than fa_bwd_noalloc's fixed array (fa_bwd_noalloc_max_bytes())";
     case FA_ERR_BAD_PAGE: return "a kernel met a page or slot outside the cache and skipped it";

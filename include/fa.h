@@ -39,8 +39,9 @@
  *     that runs out records a status readable with fa_device_status().
  *   - Thread safety: calls are re-entrant; the first call on a device also
  *     configures the kernels' shared-memory limits for that device.
- *   - CUDA graphs: the attention calls (fa_fwd*, fa_bwd*, fa_fwd_decode,
- *     fa_fwd_standard) only enqueue kernel launches on the stream, so a
+ *   - CUDA graphs: the attention calls (fa_fwd*, fa_bwd*, fa_fwd_decode*,
+ *     fa_fwd_standard), fa_rope, fa_page_tables and fa_cache_append_fp8 only
+ *     enqueue kernel launches on the stream, so a
  *     caller may capture them into a graph and replay it.  Make the first
  *     call on each device outside any capture (it looks up device attributes
  *     and symbol addresses once).  fa_bwd_events also records the caller's
@@ -71,7 +72,7 @@ typedef enum fa_status {
   FA_ERR_ARCH = 4,            /* current device is not sm_100 (B200 class) */
   FA_ERR_LAUNCH = 5,          /* CUDA runtime rejected a launch or attribute */
   FA_ERR_DEVICE_TIMEOUT = 6,  /* a bounded device wait ran out (fa_device_status) */
-  FA_ERR_WORKSPACE = 7,       /* backward workspace missing or too small */
+  FA_ERR_WORKSPACE = 7,       /* workspace missing or too small */
   FA_ERR_SCRATCH_LIMIT = 8,   /* shape needs more than fa_bwd_noalloc's fixed scratch */
   FA_ERR_BAD_PAGE = 9         /* a kernel met a page or slot outside the cache and skipped it (fa_device_status) */
 } fa_status;
@@ -370,8 +371,10 @@ FA_API fa_status fa_rope(const void* x, void* y, const int* positions, const dou
  *   seq_lens    : out, int32 [B]: new length (0 when finished); may be ctx_lens
  *   free_head_out : out, int32 [1]; may be free_head
  * A request was granted iff seq_lens[b] = ctx_lens[b] + new_lens[b].  N = 0
- * only gives pages back.  If more pages come back than ever were taken
- * (the returned ones exceed *free_head), none does and FA_ERR_BAD_PAGE is recorded.
+ * only gives pages back.  A page belongs to one request: one that stands in the
+ * rows of two finished requests (a shared prompt) would go back twice.  If more
+ * pages come back than ever were taken (the returned ones exceed *free_head),
+ * none does and FA_ERR_BAD_PAGE is recorded.
  */
 FA_API fa_status fa_page_tables(const int* ctx_lens, const int* new_lens, int* free_pages, const int* free_head,
                                 int* block_table, int* slots, int* positions, int* seq_lens, int* free_head_out,
@@ -411,12 +414,17 @@ FA_API fa_status fa_cache_append_fp8(const void* k, const void* v, const int* sl
  *   causal      : query i sees keys j <= seq_lens[b] - Nq + i
  *   workspace   : >= fa_fwd_decode_paged_fp8_workspace_size(B,H,Hkv,Nq,d) bytes
  *                 of device scratch, contents on entry ignored; not to be used
- *                 by another call that overlaps this one on the GPU
+ *                 by another call that overlaps this one on the GPU.  After
+ *                 FA_ERR_DEVICE_TIMEOUT it is to be zeroed before a captured
+ *                 call that uses it is replayed
  * A row that sees no key (length 0, or causal with i < Nq - seq_lens[b]) gets
  * O = 0 and LSE = -inf.  Bytes of the cache at or behind a request's length
  * have no effect, whatever they are.  A key or query with a NaN makes the rows
  * that see it NaN, a value's NaN those rows' outputs in its column.  The
- * scales that count must be finite, 0 or within 2^-60..2^60.
+ * scales that count must be 0 or within 2^-60..2^60.  Of keys that one row
+ * sees, one is left out of its sums where its weight times its V scale is below
+ * 2^-126 of the largest such product: with V scales of one request and head
+ * within a factor of 2^90 of one another, that is a weight below 2^-36.
  */
 FA_API fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache,
                                          const float* k_scale, const float* v_scale, const int* block_table,
