@@ -49,7 +49,7 @@
 // Measured, in a CUDA graph, H/Hkv = 4, ragged lengths up to n: B32 Hkv8 n8192
 // d128 57 us with pages of 16, 54 with 64 (301 MB, 5.3 and 5.6 TB/s; loads alone
 // 49); B8 n131072 177 us (6.65 TB/s).  32 rows (B48 Hkv8, 4 queries of 8 heads,
-// n16384, 909 MB) 187 us, 4.9 TB/s: the softmax warps issue on most cycles and
+// n16384, 909 MB) 185 us, 4.9 TB/s: the softmax warps issue on most cycles and
 // wait for one another's tiles (loads alone 132; under a sustained load at 1.68
 // GHz 230 us).  What short pieces cost is the chain from pages to output, about
 // 10 us from launch to end: B1 n1000 12.4 us, of which the launch, lengths,
@@ -69,7 +69,7 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 // What a piece costs beside its tiles, in tiles (measured: a batch of 256 x 512
-// keys takes 72 us with 0, 65 with 2).
+// keys took 72 us with 0, 65 with 2).
 constexpr int kPieceCost = 2;
 constexpr float kRescaleThreshold = 4.0f;   // log2 units
 constexpr float kBase = 2048.0f;            // P is scaled by 2^11: at most 2^15, of e5m2's 57344
@@ -874,10 +874,15 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < H; r += 4) {
             const float4 qf = *reinterpret_cast<const float4*>(&b->q_factor[qb][hr + r]);
-            s[u][r] = fmaf(s[u][r], qf.x * f.x, f.y + nm[r]);
-            s[u][r + 1] = fmaf(s[u][r + 1], qf.y * f.x, f.y + nm[r + 1]);
-            s[u][r + 2] = fmaf(s[u][r + 2], qf.z * f.x, f.y + nm[r + 2]);
-            s[u][r + 3] = fmaf(s[u][r + 3], qf.w * f.x, f.y + nm[r + 3]);
+            const float2 k2 = make_float2(f.x, f.x), v2 = make_float2(f.y, f.y);
+            const float2 x = ffma2(make_float2(s[u][r], s[u][r + 1]), fmul2(make_float2(qf.x, qf.y), k2),
+                                   fadd2(v2, make_float2(nm[r], nm[r + 1])));
+            const float2 y = ffma2(make_float2(s[u][r + 2], s[u][r + 3]), fmul2(make_float2(qf.z, qf.w), k2),
+                                   fadd2(v2, make_float2(nm[r + 2], nm[r + 3])));
+            s[u][r] = x.x;
+            s[u][r + 1] = x.y;
+            s[u][r + 2] = y.x;
+            s[u][r + 3] = y.y;
           }
           if (!there)        // whatever came of stale codes
 #pragma unroll
@@ -913,10 +918,12 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         // threshold, or has a row none yet?  One barrier with a vote; the maxima
         // themselves are only exchanged when one does.
         bool need = have != (1u << H) - 1u;
+        float most = -INFINITY;
 #pragma unroll
         for (int r = 0; r < H; ++r)
 #pragma unroll
-          for (int u = 0; u < U; ++u) need |= s[u][r] > kRescaleThreshold;
+          for (int u = 0; u < U; ++u) most = fmaxf(most, s[u][r]);
+        need |= most > kRescaleThreshold;
         if (group_any(1 + group, need)) {
 #pragma unroll
           for (int r = 0; r < H; r += 4) {
@@ -980,12 +987,14 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           uint32_t hi[H / 2], mid[H / 2], lo[H / 2];
 #pragma unroll
           for (int r = 0; r < H; r += 2) {
-            const float p0 = ex2_approx(s[u][r]), p1 = ex2_approx(s[u][r + 1]);
-            l_t[r] = fmaf(p0, inv[u], l_t[r]);
-            l_t[r + 1] = fmaf(p1, inv[u], l_t[r + 1]);
+            const float2 p2 = make_float2(ex2_approx(s[u][r]), ex2_approx(s[u][r + 1]));
+            const float2 l2 = ffma2(p2, make_float2(inv[u], inv[u]), make_float2(l_t[r], l_t[r + 1]));
+            const float2 b2 = fmul2(p2, make_float2(kBase, kBase));
+            l_t[r] = l2.x;
+            l_t[r + 1] = l2.y;
             // in fp16, then its three e5m2 parts (e5m2 is fp16's upper
             // byte; adding 0x80 rounds the magnitude to nearest)
-            const __half2 h = __floats2half2_rn(p0 * kBase, p1 * kBase);
+            const __half2 h = __floats2half2_rn(b2.x, b2.y);
             hi[r / 2] = (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xff00ff00u;
             const __half2 d1 = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hi[r / 2])), __float2half2_rn(8.0f));
             mid[r / 2] = (*reinterpret_cast<const uint32_t*>(&d1) + 0x00800080u) & 0xff00ff00u;
