@@ -49,7 +49,7 @@
 // Measured, in a CUDA graph, H/Hkv = 4, ragged lengths up to n: B32 Hkv8 n8192
 // d128 57 us with pages of 16, 54 with 64 (301 MB, 5.3 and 5.6 TB/s; loads alone
 // 49); B8 n131072 177 us (6.65 TB/s).  32 rows (B48 Hkv8, 4 queries of 8 heads,
-// n16384, 909 MB) 185 us, 4.9 TB/s: the softmax warps issue on most cycles and
+// n16384, 909 MB) 183 us, 5.0 TB/s: the softmax warps issue on most cycles and
 // wait for one another's tiles (loads alone 132; under a sustained load at 1.68
 // GHz 230 us).  What short pieces cost is the chain from pages to output, about
 // 10 us from launch to end: B1 n1000 12.4 us, of which the launch, lengths,
@@ -146,6 +146,7 @@ struct PgBarriers {
   Place start;
   uint32_t tmem_base;
   uint32_t abort;
+  uint32_t drained;                        // `abort` of the waits for copies in flight
 };
 
 template <int D, int R>
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     }
     if (lane == 0) {
       mbar_init(&b->merged, 1);
-      b->abort = 0u;
+      b->abort = b->drained = 0u;
     }
     fence_mbar_init();
   } else if (CAUSAL && warp >= S::kEpi) {
@@ -660,6 +661,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 
   // the cache is streamed once, unless several row tiles read it
   const uint64_t pol = a.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+  int loaded = 0;                                    // tiles that this warp has issued copies of
   if (n_tiles == 0) {
     // nothing but the empty requests below
   } else if (warp == 0) {
@@ -680,6 +682,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           break;
         }
         pb.load(tmK, SHARED ? nullptr : &tmV, S::kTileBytes, row, u, sKV + s * S::kStageBytes, D, &b->kv_full[s], pol);
+        loaded = t + 1;
       }
       row = next;
     }
@@ -804,10 +807,12 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
           b->page[s][pb.i] = row >= 0 ? make_float4(ks * a.c_log2, lv - ref, iv * ref2, vs)
                                       : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
         __syncwarp();
-        if (SHARED)
+        if (SHARED) {
           pb.load(tmV, nullptr, 0, row, u, sKV + s * S::kStageBytes + S::kTileBytes, D, &b->kv_full[s], pol);
-        else if (lane == 0)
+          loaded = t + 1;
+        } else if (lane == 0) {
           mbar_arrive(&b->kv_full[s]);
+        }
       }
       row = next;
       ks = row >= 0 ? a.k_scale[row] : 0.0f;
@@ -1181,6 +1186,12 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
+  }
+  if (b->abort) {
+    // A wait ran out: outputs are undefined, but no copy may outlive the CTA.
+    const WaitCtx drain{&b->drained, a.status, 1000000ull};
+    for (int t = max(0, loaded - NS); t < loaded; ++t) (void)mbar_wait(&b->kv_full[t % NS], (t / NS) & 1, drain, WAIT_PAGED_KV);
+    return;
   }
   uint32_t phase = 0;
   const int n_merge = b->n_merge;
