@@ -307,6 +307,14 @@ def _gpu_index(t):
     return t.get_device()
 
 
+def _empty(shape, stride, dtype, device, stream):
+    """A tensor of the memory of the stream that the call runs on: freed, it is next used in that stream's order."""
+    if stream is None:
+        return torch.empty_strided(shape, stride, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, stride, dtype=dtype, device=device)
+
+
 def _dims(t):
     if t.dim() != 4:
         raise ValueError("tensors must be [B, H, N, d]")
@@ -358,13 +366,13 @@ def _rope_new(x, positions, inv_freq, factor, interleaved, transpose, stream):
     B, H, N, d = _dims(x)
     dev = _gpu_index(x)
     stride = (H * N * d, N * d, d, 1)
-    y = torch.empty_strided((B, H, N, d), stride, dtype=torch.bfloat16, device=x.device)
+    y = _empty((B, H, N, d), stride, torch.bfloat16, x.device, stream)
     _rope(x, y, stride, positions, inv_freq, factor, interleaved, transpose, stream, dev)
     return y
 
 
 def rope_forward(x, positions, inv_freq, interleaved: bool = False, factor: float = 1.0, stream=None):
-    """Rotary positions on x, as a new contiguous tensor."""
+    """Rotary positions on x, as a new contiguous tensor (of `stream`'s memory, as torch.cuda.stream would give it)."""
     return _rope_new(x, positions, inv_freq, factor, interleaved, False, stream)
 
 
@@ -462,14 +470,14 @@ def _decode_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
 
 def attention_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                                scale: float | None = None, causal: bool = False, workspace=None, stream=None):
-    """Allocates O, LSE (and the workspace unless given) with torch and runs fa_fwd_decode_paged_fp8."""
+    """Allocates O, LSE (and the workspace unless given) with torch, on `stream`, and runs fa_fwd_decode_paged_fp8."""
     B, H, Nq, d = _dims(q)
     dev = _gpu_index(q)
-    o = torch.empty_like(q, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
-    lse = torch.empty_strided((B, H, Nq), (H * Nq, Nq, 1), dtype=torch.float32, device=q.device)
+    o = _empty((B, H, Nq, d), (H * Nq * d, Nq * d, d, 1), torch.bfloat16, q.device, stream)
+    lse = _empty((B, H, Nq), (H * Nq, Nq, 1), torch.float32, q.device, stream)
     if workspace is None:
         n = fa_fwd_decode_paged_fp8_workspace_size(B, H, k_cache.shape[1], Nq, d)
-        workspace = torch.empty(max(16, n), dtype=torch.uint8, device=q.device)
+        workspace = _empty((max(16, n),), (1,), torch.uint8, q.device, stream)
     _decode_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse,
                   _default_scale(d) if scale is None else scale, causal, workspace, stream, dev)
     return o, lse

@@ -632,6 +632,27 @@ def test_decode_on_two_streams():
         assert torch.equal(o, ro) and torch.equal(lse, rl)
 
 
+def test_allocating_calls_on_another_stream():
+    """What a call allocates for another stream is not handed to the current stream while it runs."""
+    q, kc, vc, ks, vs, table, lens = decode_case(16, 16, 2, 2, 128, 16, [4000 + i for i in range(16)], seed=97)
+    args = (q[1], kc[1], vc[1], ks[1], vs[1], i32(table), i32(lens))
+    x = torch.randn(4, 16, 4096, 128, device="cuda").to(torch.bfloat16)
+    freq = fa.rope_frequencies(128)[0]
+    ro, rl = fa.attention_decode_paged_fp8(*args, causal=True)
+    ry = fa.rope_backward(fa.rope_forward(x, None, freq), None, freq)
+    torch.cuda.synchronize()
+    n = fa.fa_fwd_decode_paged_fp8_workspace_size(16, 16, 2, 2, 128)
+    side, outs = torch.cuda.Stream(), []
+    for _ in range(20):
+        outs.append(fa.attention_decode_paged_fp8(*args, causal=True, stream=side))
+        y = fa.rope_backward(fa.rope_forward(x, None, freq, stream=side), None, freq, stream=side)
+        for size in (n, 2 * x.numel()):
+            torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ro) and torch.equal(lse, rl) for o, lse in outs)
+    assert torch.equal(y, ry)
+
+
 def test_empty_calls():
     z = torch.zeros
     bf, c = torch.bfloat16, "cuda"
