@@ -295,10 +295,14 @@ def _launch(fn, device: int, stream, *args):
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
+def _not_as(t, name, shape, dtypes, device):
+    raise ValueError(f"{name}: expected contiguous {' or '.join(str(x) for x in dtypes)} {tuple(shape)} on cuda:{device}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
 def _check_as(t, name, shape, dtypes, device):
     if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{name}: expected contiguous {' or '.join(str(x) for x in dtypes)} {tuple(shape)} on cuda:{device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+        _not_as(t, name, shape, dtypes, device)
 
 
 def _gpu_index(t):
@@ -307,12 +311,12 @@ def _gpu_index(t):
     return t.get_device()
 
 
-def _empty(shape, stride, dtype, device, stream):
+def _empty(like, shape, stride, dtype, stream):
     """A tensor of the memory of the stream that the call runs on: freed, it is next used in that stream's order."""
     if stream is None:
-        return torch.empty_strided(shape, stride, dtype=dtype, device=device)
+        return like.new_empty_strided(shape, stride, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty_strided(shape, stride, dtype=dtype, device=device)
+        return like.new_empty_strided(shape, stride, dtype=dtype)
 
 
 def _dims(t):
@@ -321,7 +325,8 @@ def _dims(t):
     return t.shape
 
 
-_I32, _F32, _F64, _BF16 = (torch.int32,), (torch.float32,), (torch.float64,), (torch.bfloat16,)
+_i32, _f32, _f64, _bf16 = torch.int32, torch.float32, torch.float64, torch.bfloat16
+_I32, _F32, _F64, _BF16 = (_i32,), (_f32,), (_f64,), (_bf16,)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -354,10 +359,13 @@ def _rope(x, y, y_stride, positions, inv_freq, factor, interleaved, transpose, s
     if x.dtype is not torch.bfloat16 or xd != 1:
         raise ValueError(f"x: expected bf16 with d contiguous, got {x.dtype} with strides {x.stride()}")
     if positions is not None:
-        _check_as(positions, "positions", (B, N), _I32, dev)
+        if (positions.shape != (B, N) or positions.dtype is not _i32 or not positions.is_contiguous()
+                or positions.get_device() != dev):
+            _not_as(positions, "positions", (B, N), _I32, dev)
         positions = positions.data_ptr()
     pairs = inv_freq.numel()
-    _check_as(inv_freq, "inv_freq", (pairs,), _F64, dev)
+    if inv_freq.dim() != 1 or inv_freq.dtype is not _f64 or not inv_freq.is_contiguous() or inv_freq.get_device() != dev:
+        _not_as(inv_freq, "inv_freq", (pairs,), _F64, dev)
     _launch(lib.fa_rope, dev, stream, x.data_ptr(), y.data_ptr(), positions, inv_freq.data_ptr(), factor, B, H, N, d,
             2 * pairs, 1 if interleaved else 0, 1 if transpose else 0, xb, xh, xn, y_stride[0], y_stride[1], y_stride[2])
 
@@ -366,7 +374,7 @@ def _rope_new(x, positions, inv_freq, factor, interleaved, transpose, stream):
     B, H, N, d = _dims(x)
     dev = _gpu_index(x)
     stride = (H * N * d, N * d, d, 1)
-    y = _empty((B, H, N, d), stride, torch.bfloat16, x.device, stream)
+    y = _empty(x, (B, H, N, d), stride, None, stream)      # bf16, or refused below
     _rope(x, y, stride, positions, inv_freq, factor, interleaved, transpose, stream, dev)
     return y
 
@@ -392,12 +400,14 @@ def fa_page_tables(ctx_lens, new_lens, free_pages, free_head, block_table, slots
     B, N = slots.shape
     max_pages = block_table.shape[1]
     n_free = free_pages.numel()
-    for t, name, shape in ((ctx_lens, "ctx_lens", (B,)), (new_lens, "new_lens", (B,)),
-                           (free_pages, "free_pages", (n_free,)), (free_head, "free_head", (1,)),
-                           (block_table, "block_table", (B, max_pages)), (slots, "slots", (B, N)),
-                           (positions, "positions", (B, N)), (seq_lens, "seq_lens", (B,)),
-                           (free_head_out, "free_head_out", (1,))):
-        _check_as(t, name, shape, _I32, dev)
+    # one look at what all have in common, then the shapes
+    for t in (ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens, free_head_out):
+        if t.dtype is not _i32 or not t.is_contiguous() or t.get_device() != dev:
+            _not_as(t, "every argument", t.shape, _I32, dev)
+    if (ctx_lens.shape != (B,) or new_lens.shape != (B,) or free_pages.dim() != 1 or free_head.shape != (1,)
+            or block_table.shape[0] != B or positions.shape != (B, N) or seq_lens.shape != (B,) or free_head_out.shape != (1,)):
+        raise ValueError("expected ctx_lens, new_lens, seq_lens [B], free_pages [n_free], free_head, free_head_out [1], "
+                         f"block_table [B, max_pages], slots, positions [B, N] with [B, N] = {[B, N]}")
     _launch(lib.fa_page_tables, dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
                free_head.data_ptr(), block_table.data_ptr(), slots.data_ptr(), positions.data_ptr(),
                seq_lens.data_ptr(), free_head_out.data_ptr(), B, N, n_free, max_pages, page_size)
@@ -409,10 +419,15 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev):
     pages, heads, page, depth = shape = k_cache.shape
     if heads != Hkv or depth != d:
         raise ValueError(f"k_cache: expected [num_pages, {Hkv}, page_size, {d}], got {tuple(shape)}")
-    _check_as(k_cache, "k_cache", shape, _E4M3, dev)
-    _check_as(v_cache, "v_cache", shape, _E4M3, dev)
-    _check_as(k_scale, "k_scale", (pages, Hkv), _F32, dev)
-    _check_as(v_scale, "v_scale", (pages, Hkv), _F32, dev)
+    if k_cache.dtype not in _E4M3 or not k_cache.is_contiguous() or k_cache.get_device() != dev:
+        _not_as(k_cache, "k_cache", shape, _E4M3, dev)
+    if v_cache.shape != shape or v_cache.dtype not in _E4M3 or not v_cache.is_contiguous() or v_cache.get_device() != dev:
+        _not_as(v_cache, "v_cache", shape, _E4M3, dev)
+    scales = (pages, Hkv)
+    if k_scale.shape != scales or k_scale.dtype is not _f32 or not k_scale.is_contiguous() or k_scale.get_device() != dev:
+        _not_as(k_scale, "k_scale", scales, _F32, dev)
+    if v_scale.shape != scales or v_scale.dtype is not _f32 or not v_scale.is_contiguous() or v_scale.get_device() != dev:
+        _not_as(v_scale, "v_scale", scales, _F32, dev)
     return pages, page
 
 
@@ -421,9 +436,12 @@ def fa_cache_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=
     k_cache, v_cache e4m3 [num_pages,Hkv,page_size,d], k_scale, v_scale fp32 [num_pages,Hkv]."""
     B, Hkv, N, d = shape = _dims(k)
     dev = _gpu_index(k)
-    _check_as(k, "k", shape, _BF16, dev)
-    _check_as(v, "v", shape, _BF16, dev)
-    _check_as(slots, "slots", (B, N), _I32, dev)
+    if k.dtype is not _bf16 or not k.is_contiguous():
+        _not_as(k, "k", shape, _BF16, dev)
+    if v.shape != shape or v.dtype is not _bf16 or not v.is_contiguous() or v.get_device() != dev:
+        _not_as(v, "v", shape, _BF16, dev)
+    if slots.shape != (B, N) or slots.dtype is not _i32 or not slots.is_contiguous() or slots.get_device() != dev:
+        _not_as(slots, "slots", (B, N), _I32, dev)
     pages, page = _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
     _launch(lib.fa_cache_append_fp8, dev, stream, k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
                v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, Hkv, N, d, pages, page)
@@ -450,14 +468,18 @@ def fa_fwd_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
 def _decode_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, scale, causal, workspace, stream,
                   dev):
     B, H, Nq, d = shape = q.shape
-    _check_as(q, "q", shape, _BF16, dev)
+    if q.dtype is not _bf16 or not q.is_contiguous():
+        _not_as(q, "q", shape, _BF16, dev)
     if k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_cache must be [num_pages, Hkv, page_size, d] and block_table [B, max_pages]")
     Hkv = k_cache.shape[1]
     pages, page = _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
     max_pages = block_table.shape[1]
-    _check_as(block_table, "block_table", (B, max_pages), _I32, dev)
-    _check_as(seq_lens, "seq_lens", (B,), _I32, dev)
+    if (block_table.shape[0] != B or block_table.dtype is not _i32 or not block_table.is_contiguous()
+            or block_table.get_device() != dev):
+        _not_as(block_table, "block_table", (B, max_pages), _I32, dev)
+    if seq_lens.shape != (B,) or seq_lens.dtype is not _i32 or not seq_lens.is_contiguous() or seq_lens.get_device() != dev:
+        _not_as(seq_lens, "seq_lens", (B,), _I32, dev)
     wptr, wbytes = 0, 0
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -473,11 +495,11 @@ def attention_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     """Allocates O, LSE (and the workspace unless given) with torch, on `stream`, and runs fa_fwd_decode_paged_fp8."""
     B, H, Nq, d = _dims(q)
     dev = _gpu_index(q)
-    o = _empty((B, H, Nq, d), (H * Nq * d, Nq * d, d, 1), torch.bfloat16, q.device, stream)
-    lse = _empty((B, H, Nq), (H * Nq, Nq, 1), torch.float32, q.device, stream)
+    o = _empty(q, (B, H, Nq, d), (H * Nq * d, Nq * d, d, 1), None, stream)      # bf16, or refused below
+    lse = _empty(q, (B, H, Nq), (H * Nq, Nq, 1), _f32, stream)
     if workspace is None:
         n = fa_fwd_decode_paged_fp8_workspace_size(B, H, k_cache.shape[1], Nq, d)
-        workspace = _empty((max(16, n),), (1,), torch.uint8, q.device, stream)
+        workspace = _empty(q, (max(16, n),), (1,), torch.uint8, stream)
     _decode_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse,
                   _default_scale(d) if scale is None else scale, causal, workspace, stream, dev)
     return o, lse

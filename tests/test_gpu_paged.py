@@ -653,6 +653,30 @@ def test_allocating_calls_on_another_stream():
     assert torch.equal(y, ry)
 
 
+def test_python_calls_refuse_tensors_that_do_not_fit():
+    """Each tensor of a call in turn with another type, another shape or not contiguous: refused before any launch."""
+    bf, i4, f4, u1 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+    t = lambda dtype, *shape: torch.zeros(*shape, dtype=dtype, device="cuda")
+    q, kv, slots, cache, scale = t(bf, 2, 4, 3, 64), t(bf, 2, 2, 3, 64), t(i4, 2, 3), t(u1, 5, 2, 16, 64), t(f4, 5, 2)
+    table, two, one, free, lse = t(i4, 2, 2), t(i4, 2), t(i4, 1), t(i4, 5), t(f4, 2, 4, 3)
+    work = t(u1, fa.fa_fwd_decode_paged_fp8_workspace_size(2, 4, 2, 3, 64))
+    calls = [(fa.fa_cache_append_fp8, (kv, kv, slots, cache, cache, scale, scale), ()),
+             (fa.fa_page_tables, (two, two, free, one, table, slots, slots, two, one), (16,)),
+             (lambda *a: fa.fa_fwd_decode_paged_fp8(*a, 0.1, False, work), (q, cache, cache, scale, scale, table, two, q, lse), ()),
+             (lambda q, *a: fa.fa_rope(q, q, *a), (q, slots, t(torch.float64, 32)), ())]
+    for fn, args, rest in calls:
+        fn(*(a.clone() for a in args), *rest)
+        for n, a in enumerate(args):
+            apart = torch.zeros(*a.shape[:-1], 2 * a.shape[-1], dtype=a.dtype, device="cuda")[..., ::2]
+            bads = [a.to(torch.int64), a.cpu(), a[None]]
+            if not apart.is_contiguous():              # one element is, whatever its stride
+                bads.append(apart)
+            for bad in bads:
+                with pytest.raises(ValueError):
+                    fn(*args[:n], bad, *args[n + 1:], *rest)
+    torch.cuda.synchronize()
+
+
 def test_empty_calls():
     z = torch.zeros
     bf, c = torch.bfloat16, "cuda"
