@@ -1034,16 +1034,16 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       // (by a group that had a tile, and with it waited for the piece's queries)
       if (ok && began && part == 0 && wq == 0 && lane == 0) b->stat_ref[ob] = b->page_ref[qb];
       if (ok && lane == 0) mbar_arrive(&b->q_empty[qb]);
-      if (ok && began) {
+      if (ok) {
+        // Without a tile, or without a key that is there, the maximum is -inf and
+        // the sum 0; scores that are all NaN leave no maximum either, but a NaN in
+        // the sum of whichever warp had them.
         const float l = rows_sum<H>(l_t, lane);      // of row lane / (32 / H)
         if (lane % (32 / H) == 0) b->stat_l[ob][turn][wq][hr + lane / (32 / H)] = l;
         if (wq == 0 && lane == 0) {
-          // scores that are all NaN leave no maximum, but a sum to be seen
 #pragma unroll
-          for (int r = 0; r < H; ++r) b->stat_m[ob][turn][hr + r] = (have >> r) & 1u ? -nm[r] : l_t[r] == l_t[r] ? -INFINITY : 0.0f;
+          for (int r = 0; r < H; ++r) b->stat_m[ob][turn][hr + r] = (have >> r) & 1u ? -nm[r] : -INFINITY;
         }
-      } else if (ok && wq == 0 && lane < H) {
-        b->stat_m[ob][turn][hr + lane] = -INFINITY;  // no tile of the piece: the sums are not looked at
       }
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&b->stats_full[ob]);
@@ -1081,8 +1081,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
         for (int k = 0; k < S::kTurns; ++k) {
           const float m = b->stat_m[ob][k][lane];
           f[k] = m == -INFINITY ? 0.0f : ex2_approx(m - M);
-          if (m != -INFINITY)
-            L = fmaf(f[k], b->stat_l[ob][k][0][lane] + b->stat_l[ob][k][1][lane] + b->stat_l[ob][k][2][lane] + b->stat_l[ob][k][3][lane], L);
+          L = fmaf(f[k], b->stat_l[ob][k][0][lane] + b->stat_l[ob][k][1][lane] + b->stat_l[ob][k][2][lane] + b->stat_l[ob][k][3][lane], L);
         }
         const float inv = L == 0.0f ? 0.0f : b->stat_ref[ob] * (1.0f / kBase) / L;
 #pragma unroll
