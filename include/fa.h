@@ -421,7 +421,8 @@ FA_API fa_status fa_cache_append_fp8(const void* k, const void* v, const int* sl
  * O = 0 and LSE = -inf.  Bytes of the cache at or behind a request's length
  * have no effect, whatever they are.  A key or query with a NaN makes the rows
  * that see it NaN, a value's NaN those rows' outputs in its column.  The
- * scales that count must be 0 or within 2^-60..2^60.  Of keys that one row
+ * scales that count must be 0 or within 2^-60..2^60; a NaN scale, or a negative
+ * V scale, shows as NaN in the rows that see a key of its page.  Of keys that one row
  * sees, one is left out of its sums where its weight times its V scale is below
  * 2^-126 of the largest such product: with V scales of one request and head
  * within a factor of 2^90 of one another, that is a weight below 2^-36.

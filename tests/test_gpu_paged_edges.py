@@ -45,3 +45,18 @@ def test_decode_rows_that_see_only_nan_behind_skipped_pages(what, d):
             x[r] = np.nan
     check_decode(q, kc, vc, ks, vs, table, lens, d ** -0.5, False, d, want=ref)
     assert fa.fa_device_status()[0] == fa.STATUS_CODES["FA_ERR_BAD_PAGE"]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [np.nan, -1.0])
+@pytest.mark.parametrize("at", [0, 7])
+def test_decode_value_scale_that_is_no_scale(at, bad, d):
+    """A V scale that is NaN or negative shows as NaN in the rows that see its page, and in no others."""
+    q, kc, vc, ks, vs, table, lens = decode_case(2, 4, 2, 3, d, 16, [113, 400], seed=202, stale=False)
+    vs[0][table[0, at], 1] = bad                        # page 7 holds key 112, which the last query alone sees
+    vs[1][int(table[0, at]), 1] = bad
+    fine = np.where(np.isnan(vs[0]) | (vs[0] < 0), 1.0, vs[0])
+    ref = paged.decode_paged(q[0], kc[0], vc[0], ks[0], fine, table, lens, d ** -0.5, True)
+    for x in ref:
+        x[0, 2:, 2 if at == 7 else slice(None)] = np.nan
+    check_decode(q, kc, vc, ks, vs, table, lens, d ** -0.5, True, d, want=ref)
