@@ -17,11 +17,15 @@
 //                   query (elements below 2^-10 of the row's largest, and far
 //                   below, keep 2^-21 of it).
 //   O^T += V^T P^T  d x rows (A = V tile, MN-major).  p * vs is rounded to fp16
-//                   and split into three e5m2 parts, hi + mid/8 + lo/64, which
-//                   is exact: 11 bits in three times 3 plus the signs.  e5m2 has
-//                   fp16's exponent range, so a key down to 2^-28 of the largest
-//                   keeps its 11 bits.  A and B of one product may differ in
-//                   type among the 8-bit floats.
+//                   and split into three e5m2 parts, hi + mid/8 + lo/64: 11 bits
+//                   in three times 3 plus the signs.  The last step of lo is
+//                   2^-22 where the maximum in use is 2^11, so the split is exact
+//                   from 2^-23 of that maximum on; below, p * vs is rounded to
+//                   multiples of 2^-33 of it and under 2^-34 is gone.  The
+//                   maximum in use is at most the largest p * vs of the row, V
+//                   scales included: a column in which heavy keys are 0 has of
+//                   light ones what this leaves.  A and B of one product may
+//                   differ in type among the 8-bit floats.
 // A page's K scale multiplies its keys' scores; its V scale goes into the
 // exponent (t = s + log2 vs, P = exp2(t - m)), so that the parts cannot overflow
 // whatever the scales are, and l sums exp2(t - m) / vs.  t counts from a whole

@@ -423,9 +423,14 @@ FA_API fa_status fa_cache_append_fp8(const void* k, const void* v, const int* sl
  * that see it NaN, a value's NaN those rows' outputs in its column.  The
  * scales that count must be 0 or within 2^-60..2^60; a NaN scale, or a negative
  * V scale, shows as NaN in the rows that see a key of its page.  Of keys that one row
- * sees, one is left out of its sums where its weight times its V scale is below
- * 2^-126 of the largest such product: with V scales of one request and head
- * within a factor of 2^90 of one another, that is a weight below 2^-36.
+ * sees, one is left out of LSE, and of the sum that O is divided by, where its
+ * weight times its V scale is below 2^-126 of the largest such product: with V
+ * scales of one request and head within a factor of 2^90 of one another, that is
+ * a weight below 2^-36.  In O's sum over the values themselves, weight times V
+ * scale has 11 bits down to 2^-23 of the largest such product and is rounded to
+ * multiples of 2^-33 of it at the coarsest below; under 2^-34 of it a key may be
+ * gone.  A column of O in which only such light keys have codes other than 0 has
+ * no more bits than that.
  */
 FA_API fa_status fa_fwd_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache,
                                          const float* k_scale, const float* v_scale, const int* block_table,

@@ -60,3 +60,49 @@ def test_decode_value_scale_that_is_no_scale(at, bad, d):
     for x in ref:
         x[0, 2:, 2 if at == 7 else slice(None)] = np.nan
     check_decode(q, kc, vc, ks, vs, table, lens, d ** -0.5, True, d, want=ref)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("below", [0, 10, 20, 26, 30, 44])
+@pytest.mark.parametrize("Nq", [1, 4])
+def test_decode_columns_that_only_light_keys_fill(Nq, below, d):
+    """Half of the columns are zero in the pages of a large V scale, so that the others, 2^-below of it, alone count
+    there.  A weight times its V scale is rounded to 11 bits (in the usual tolerance), and by at most 2^-23 + 2^-25 where
+    the maximum in use is 2^11: 1.25 * 2^-34 of the largest product of the row, times the key's code."""
+    q, kc, vc, ks, vs, table, lens = decode_case(2, 8, 2, Nq, d, 16, [900, 300], seed=203, q_mult=0.25, stale=False)
+    heavy = np.zeros(vs[0].shape[0], bool)
+    heavy[table[:, ::2]] = True                         # every tile has pages of both kinds
+    vs[0][:] = np.where(heavy[:, None], 1.0, 2.0 ** -below)
+    vc[0][heavy, :, :, : d // 2] = 0
+    upload((vs[0], vs[1]), (vc[0], vc[1]))
+    scale = d ** -0.5
+    ref = paged.decode_paged(q[0], kc[0], vc[0], ks[0], vs[0], table, lens, scale, False)
+    o, _ = (gu.to_f64(t) for t in check_decode_floor(q, kc, vc, ks, vs, table, lens, scale, d, ref))
+    light = np.abs(ref[0][..., : d // 2])
+    if below == 44:
+        assert np.all(o[..., : d // 2] == 0)            # below half of the last step, 2^-34: gone, and documented as such
+    if below <= 20:                                     # 11 bits, but for rounding errors of sums that cancel
+        assert np.median(np.abs(o[..., : d // 2] - ref[0][..., : d // 2]) / light) <= 2.0 ** -8
+
+
+def check_decode_floor(q, kc, vc, ks, vs, table, lens, scale, d, ref):
+    o, lse, mag, big = ref
+    B, H, Nq, _ = q[0].shape
+    page, Hkv = kc[0].shape[2], kc[0].shape[1]
+    floor = np.zeros_like(o)
+    for b in range(B):
+        j = np.arange(lens[b])
+        p, r = table[b, j // page], j % page
+        for h in range(H):
+            hk = h // (H // Hkv)
+            K, C, w = paged.E4M3[kc[0][p, hk, r]] * ks[0][p, hk][:, None], paged.E4M3[vc[0][p, hk, r]], vs[0][p, hk]
+            s = scale * (K @ q[0][b, h].T)
+            top = (np.exp(s - lse[b, h]) * w[:, None]).max(0)
+            floor[b, h] = 1.25 * 2.0 ** -34 * top[:, None] * np.abs(C).sum(0)
+    got = fa.attention_decode_paged_fp8(q[1], kc[1], vc[1], ks[1], vs[1], i32(table), i32(lens), scale)
+    e = (d + 8) * 2.0 ** -23 * big + 2.0 ** -20
+    assert np.all(np.abs(gu.to_f64(got[1]) - lse) <= e + 2.0 ** -23 * np.abs(lse))
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2.0 ** -14 + 2 * e[..., None]) * mag + floor + 1e-38
+    worst = np.max(np.abs(gu.to_f64(got[0]) - o) / tol)
+    assert worst <= 1, f"O off by {worst:.3g} of its bound"
+    return got
