@@ -330,11 +330,14 @@ _I32, _F32, _F64, _BF16 = (_i32,), (_f32,), (_f64,), (_bf16,)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
-                     original_length: float = 0.0, low: float = 1.0, high: float = 4.0, device="cuda"):
+                     original_length: float = 0.0, low: float = 1.0, high: float | None = None, device="cuda"):
     """(inv_freq, attention factor) of rotary positions: inv_freq is an fp64 tensor [rot_dim / 2] on `device`,
-    radians per position.  scaling is a key of ROPE_SCALINGS (see fa_rope_scaling in fa.h)."""
+    radians per position.  scaling is a key of ROPE_SCALINGS (see fa_rope_scaling in fa.h); `high` is 32 turns for
+    "yarn" and 4 for "bands" unless given."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
     out = (ctypes.c_double * max(1, rot_dim // 2))()
     att = ctypes.c_double()
     check(lib.fa_rope_frequencies(out, ctypes.byref(att), rot_dim, base, ROPE_SCALINGS[scaling], factor,
