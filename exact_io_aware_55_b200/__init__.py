@@ -393,10 +393,11 @@ def rope_backward(dy, positions, inv_freq, interleaved: bool = False, factor: fl
 
 
 def fa_page_tables(ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens,
-                   free_head_out, page_size: int, stream=None) -> None:
+                   free_head_out, page_size: int, stream=None, held_pages=None) -> None:
     """Grows (new_lens >= 0) or finishes (new_lens < 0) the requests of a batch: takes pages from free_pages,
     writes block_table, slots, positions, seq_lens and free_head_out.  All int32; seq_lens may be ctx_lens and
-    free_head_out may be free_head."""
+    free_head_out may be free_head.  held_pages [B] (read and written) counts each request's pages; it is needed
+    where ctx_lens is lowered across a page's border between calls, whose page would be lost otherwise."""
     dev = _gpu_index(ctx_lens)
     if slots.dim() != 2 or block_table.dim() != 2:
         raise ValueError("slots must be [B, N] and block_table [B, max_pages]")
@@ -411,9 +412,13 @@ def fa_page_tables(ctx_lens, new_lens, free_pages, free_head, block_table, slots
             or block_table.shape[0] != B or positions.shape != (B, N) or seq_lens.shape != (B,) or free_head_out.shape != (1,)):
         raise ValueError("expected ctx_lens, new_lens, seq_lens [B], free_pages [n_free], free_head, free_head_out [1], "
                          f"block_table [B, max_pages], slots, positions [B, N] with [B, N] = {[B, N]}")
-    _launch(lib.fa_page_tables, dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
-               free_head.data_ptr(), block_table.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-               seq_lens.data_ptr(), free_head_out.data_ptr(), B, N, n_free, max_pages, page_size)
+    args = (ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(), block_table.data_ptr(),
+            slots.data_ptr(), positions.data_ptr(), seq_lens.data_ptr(), free_head_out.data_ptr())
+    if held_pages is None:
+        _launch(lib.fa_page_tables, dev, stream, *args, B, N, n_free, max_pages, page_size)
+    else:
+        _check_as(held_pages, "held_pages", (B,), _I32, dev)
+        _launch(lib.fa_page_tables_held, dev, stream, *args, held_pages.data_ptr(), B, N, n_free, max_pages, page_size)
 
 
 def _check_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev):

@@ -83,6 +83,8 @@ def _load() -> ctypes.CDLL:
     lib.fa_rope.restype = i
     lib.fa_page_tables.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
     lib.fa_page_tables.restype = i
+    lib.fa_page_tables_held.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
+    lib.fa_page_tables_held.restype = i
     lib.fa_cache_append_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp]
     lib.fa_cache_append_fp8.restype = i
     lib.fa_fwd_decode_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, vp, sz,

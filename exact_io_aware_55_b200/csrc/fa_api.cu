@@ -755,6 +755,13 @@ fa_status fa_rope(const void* x, void* y, const int* positions, const double* in
 fa_status fa_page_tables(const int* ctx_lens, const int* new_lens, int* free_pages, const int* free_head,
                          int* block_table, int* slots, int* positions, int* seq_lens, int* free_head_out, int B,
                          int N, int n_free, int max_pages, int page_size, void* stream) {
+  return fa_page_tables_held(ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens,
+                             free_head_out, nullptr, B, N, n_free, max_pages, page_size, stream);
+}
+
+fa_status fa_page_tables_held(const int* ctx_lens, const int* new_lens, int* free_pages, const int* free_head,
+                              int* block_table, int* slots, int* positions, int* seq_lens, int* free_head_out,
+                              int* held_pages, int B, int N, int n_free, int max_pages, int page_size, void* stream) {
   if (B < 0 || N < 0 || n_free < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
   if (!page_ok(page_size)) return FA_ERR_UNSUPPORTED;
   // lengths, and the pages that a batch asks for or gives back, are counted in 32 bits
@@ -765,14 +772,15 @@ fa_status fa_page_tables(const int* ctx_lens, const int* new_lens, int* free_pag
   if (!ctx_lens || !new_lens || !free_head || !seq_lens || !free_head_out) return FA_ERR_INVALID_ARG;
   if ((N > 0 && (!slots || !positions)) || (n_free > 0 && !free_pages) || (max_pages > 0 && !block_table))
     return FA_ERR_INVALID_ARG;
-  const void* every[] = {ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens, free_head_out};
+  const void* every[] = {ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens, free_head_out,
+                         held_pages};
   for (const void* p : every)
     if (!aligned(p, 4)) return FA_ERR_ALIGNMENT;
   uint32_t* status = nullptr;
   const fa_status st = current_device(&status);
   if (st != FA_OK) return st;
   const fa::TableArgs a{status, ctx_lens, new_lens, free_pages, free_head, block_table, slots, positions, seq_lens,
-                        free_head_out, B, N, n_free, max_pages, page_size};
+                        free_head_out, held_pages, B, N, n_free, max_pages, page_size};
   return launch_status(fa::launch_page_tables(a, static_cast<cudaStream_t>(stream)));
 }
 

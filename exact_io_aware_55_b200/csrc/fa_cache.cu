@@ -250,8 +250,8 @@ cudaError_t launch_append_t(AppendArgs a, cudaStream_t stream) {
   return launch_dependent(cache_append_kernel<D, PAGE>, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0, stream, a);
 }
 
-// Page tables of a batch.  Request b holds ceil(ctx / P) pages and wants to
-// grow by new_lens[b] tokens, or (negative) has finished.  Pages of finished
+// Page tables of a batch.  Request b holds ceil(ctx / P) pages (or more, where
+// the caller keeps their number, see held_pages) and wants to grow by new_lens[b] tokens, or (negative) has finished.  Pages of finished
 // requests go in front of the free ones; then requests take pages in order:
 // request b is granted when need = 0 or the needs up to and with b still fit.
 // Two prefix sums over the batch, taken together in the halves of one 64-bit
@@ -316,11 +316,12 @@ __global__ void __launch_bounds__(kTabThreads) __cluster_dims__(kTabCluster, 1, 
     const int nw = a.new_lens[b];
     row.ctx = min(max(a.ctx_lens[b], 0), cap);
     row.held = (row.ctx + P - 1) >> shift;
+    if (a.held_pages) row.held = min(max(a.held_pages[b], row.held), a.max_pages);
     finished = nw < 0;
     if (finished) back = row.held;
     if (nw >= 0 && nw <= a.N && nw <= cap - row.ctx) {
       row.nw = nw;
-      row.need = ((row.ctx + nw + P - 1) >> shift) - row.held;
+      row.need = max(((row.ctx + nw + P - 1) >> shift) - row.held, 0);
     }
   };
   unsigned long long end = 0, total = 0, carry = 0;
@@ -391,7 +392,10 @@ __global__ void __launch_bounds__(kTabThreads) __cluster_dims__(kTabCluster, 1, 
     }
     s_row[threadIdx.x] = row;
     const int b = base + threadIdx.x;
-    if (b < a.B && rank == 0) a.seq_lens[b] = finished ? 0 : row.ctx + max(row.nw, 0);
+    if (b < a.B && rank == 0) {
+      a.seq_lens[b] = finished ? 0 : row.ctx + max(row.nw, 0);
+      if (a.held_pages) a.held_pages[b] = finished ? 0 : row.held + row.need;
+    }
     if (asked <= avail && threadIdx.x == 0) s_taken = static_cast<int>(asked);
     __syncthreads();
     const int rows = min(kTabThreads, a.B - base);

@@ -256,6 +256,7 @@ struct TableArgs {
   int* positions;        // [B, N]
   int* seq_lens;         // [B]
   int* free_head_out;
+  int* held_pages;       // [B] in/out, or NULL: as many as hold ctx_lens
   int B, N, n_free, max_pages, page;
 };
 cudaError_t launch_page_tables(const TableArgs& a, cudaStream_t stream);

@@ -374,11 +374,29 @@ FA_API fa_status fa_rope(const void* x, void* y, const int* positions, const dou
  * only gives pages back.  A page belongs to one request: one that stands in the
  * rows of two finished requests (a shared prompt) would go back twice.  If more
  * pages come back than ever were taken (the returned ones exceed *free_head),
- * none does and FA_ERR_BAD_PAGE is recorded.
+ * none does and FA_ERR_BAD_PAGE is recorded.  A request holds the pages of
+ * ctx_lens and no others, so a caller that lowers ctx_lens across a page's border
+ * (rejected tokens of a draft) loses the page behind it: fa_page_tables_held is
+ * for that.
  */
 FA_API fa_status fa_page_tables(const int* ctx_lens, const int* new_lens, int* free_pages, const int* free_head,
                                 int* block_table, int* slots, int* positions, int* seq_lens, int* free_head_out,
                                 int B, int N, int n_free, int max_pages, int page_size, void* stream);
+
+/*
+ * fa_page_tables for requests that may also shrink between calls.
+ *   held_pages  : in/out, int32 [B]: how many entries of its row of block_table
+ *                 are the request's (0 for a new one), at least the pages of
+ *                 ctx_lens[b] and at most max_pages (another number counts as the
+ *                 nearest of these); or NULL, for fa_page_tables
+ * Pages behind a lowered ctx_lens[b] stay the request's: new tokens go into them
+ * before pages are taken, and they go back with the others when it has finished.
+ * held_pages[b] gets the number after the call, 0 for a finished request.
+ */
+FA_API fa_status fa_page_tables_held(const int* ctx_lens, const int* new_lens, int* free_pages, const int* free_head,
+                                     int* block_table, int* slots, int* positions, int* seq_lens, int* free_head_out,
+                                     int* held_pages, int B, int N, int n_free, int max_pages, int page_size,
+                                     void* stream);
 
 /*
  * Writes new keys and values into the 8-bit cache.

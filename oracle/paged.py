@@ -93,12 +93,17 @@ def append(k, v, slots, k_codes, v_codes, k_scale, v_scale, page):
                     scale[p, h] = now
 
 
-def page_tables(ctx, new, free, head, table, N, page):
-    """(table, free, slots, positions, lens, head) after the step; nothing of the inputs is changed."""
+def page_tables(ctx, new, free, head, table, N, page, held=None):
+    """(table, free, slots, positions, lens, head) after the step; nothing of the inputs is changed but `held`, the
+    number of each request's pages where lengths may have been lowered."""
     table, free, head = table.copy(), free.copy(), int(head)
     B, per_row = table.shape
     slots, pos, lens = np.full((B, N), -1), np.zeros((B, N), int), ctx.copy()
-    back = [p for b in range(B) if new[b] < 0 for p in table[b, : -(-int(ctx[b]) // page)]]
+    has = [-(-int(n) // page) for n in ctx]
+    if held is not None:
+        has = [min(max(int(held[b]), has[b]), per_row) for b in range(B)]
+        held[:] = [0 if new[b] < 0 else has[b] for b in range(B)]
+    back = [p for b in range(B) if new[b] < 0 for p in table[b, : has[b]]]
     if len(back) <= head:
         head -= len(back)
         free[head:head + len(back)] = back
@@ -107,15 +112,16 @@ def page_tables(ctx, new, free, head, table, N, page):
         if new[b] < 0:
             lens[b] = 0
             continue
-        held = -(-int(ctx[b]) // page)
         if new[b] > N or ctx[b] + new[b] > per_row * page:
             continue
-        need = -(-int(ctx[b] + new[b]) // page) - held
+        need = max(-(-int(ctx[b] + new[b]) // page) - has[b], 0)
         asked += need
         if need and asked > avail:
             continue
         for i in range(need):
-            table[b, held + i] = free[head + asked - need + i]
+            table[b, has[b] + i] = free[head + asked - need + i]
+        if held is not None:
+            held[b] += need
         taken += need
         for t in range(int(new[b])):
             at = int(ctx[b]) + t

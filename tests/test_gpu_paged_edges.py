@@ -106,3 +106,43 @@ def check_decode_floor(q, kc, vc, ks, vs, table, lens, scale, d, ref):
     worst = np.max(np.abs(gu.to_f64(got[0]) - o) / tol)
     assert worst <= 1, f"O off by {worst:.3g} of its bound"
     return got
+
+
+@pytest.mark.parametrize("B,N,page,pages", [(1, 5, 16, 6), (5, 40, 16, 30), (33, 3, 32, 25), (2500, 2, 16, 4000), (3, 700, 128, 40)])
+def test_page_tables_of_requests_that_shrink(B, N, page, pages):
+    """Lengths lowered between calls (rejected drafts), across pages' borders too: every call as the oracle's, and no page
+    is lost or in two places."""
+    rng = np.random.default_rng(B + N)
+    per_row = max(3, -(-4 * N // page))
+    table, free, head, ctx = np.full((B, per_row), -1), rng.permutation(pages), 0, np.zeros(B, int)
+    held, held_t = np.zeros(B, int), torch.zeros(B, dtype=torch.int32, device="cuda")
+    for _ in range(8):
+        new = rng.integers(0, N + 1, B)
+        new[rng.random(B) < 0.1] = -1
+        new[rng.random(B) < 0.05] = N + 1
+        c, f, h, t = i32(ctx), i32(free), i32([head]), i32(table)
+        slots, pos = (torch.empty(B, N, dtype=torch.int32, device="cuda") for _ in range(2))
+        fa.fa_page_tables(c, i32(new), f, h, t, slots, pos, c, h, page, held_pages=held_t)
+        table, free, wslots, wpos, ctx, head = paged.page_tables(ctx, new, free, head, table, N, page, held)
+        for got, want in ((slots, wslots), (pos, wpos), (c, ctx), (h, [head]), (t, table), (f, free), (held_t, held)):
+            assert np.array_equal(got.cpu().numpy(), np.asarray(want))
+        own = [p for b in range(B) for p in table[b, :held[b]]] + list(free[head:])
+        assert sorted(own) == list(range(pages))
+        ctx = np.maximum(ctx - rng.integers(0, 2 * N, B), 0)
+
+
+def test_page_tables_held_counts_out_of_range():
+    """A count below the length's pages, or beyond the row, is the nearest possible one; other tensors are refused."""
+    table, free = np.arange(8).reshape(2, 4), np.arange(8, 16)
+    ctx, new, held = np.array([20, 5]), np.array([30, 3]), np.array([-7, 10 ** 6])
+    held_t, t, f, h = i32(held), i32(table), i32(free), i32([4])
+    slots, pos, seq = (torch.empty(*s, dtype=torch.int32, device="cuda") for s in ((2, 32), (2, 32), (2,)))
+    args = (i32(ctx), i32(new), f, h, t, slots, pos, seq, h, 16)
+    fa.fa_page_tables(*args, held_pages=held_t)
+    table, free, wslots, _, lens, head = paged.page_tables(ctx, new, free, 4, table, 32, 16, held)
+    assert list(held) == [4, 4] and head == 6
+    for got, want in ((slots, wslots), (seq, lens), (h, [head]), (t, table), (held_t, held)):
+        assert np.array_equal(got.cpu().numpy(), np.asarray(want))
+    for bad in (held_t.long(), held_t[:1], held_t.cpu(), held_t[None]):
+        with pytest.raises(ValueError):
+            fa.fa_page_tables(*args, held_pages=bad)
