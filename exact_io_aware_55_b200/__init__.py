@@ -458,7 +458,7 @@ def fa_cache_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=
 def fa_fwd_decode_paged_fp8_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int) -> int:
     n = int(lib.fa_fwd_decode_paged_fp8_workspace_size(B, H, Hkv, Nq, d))
     if n == ctypes.c_size_t(-1).value:
-        raise FAError(1, "invalid shape for fa_fwd_decode_paged_fp8_workspace_size")
+        raise FAError(1, "invalid or unsupported shape for fa_fwd_decode_paged_fp8_workspace_size")
     return n
 
 

@@ -593,6 +593,12 @@ namespace {
 // Shape checks of the calls on the 8-bit paged cache and of fa_rope.
 bool page_ok(int page_size) { return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128; }
 
+// Requests and heads of a batch: the dense calls' limit, or more heads than that
+// for up to 8192 requests (no grid of these kernels has a dimension of B times H).
+bool batch_fits(int B, int H) {
+  return static_cast<long long>(B) * H <= 65535 || (B <= 8192 && H <= 65535);
+}
+
 // num_pages * Hkv rows of page_size * d bytes: the tensor maps index
 // (page, head) pairs and a slot in 32 bits.
 bool cache_fits(int num_pages, int Hkv, int page_size) {
@@ -658,7 +664,7 @@ fa_status check_paged(int B, int H, int Hkv, int Nq, int d, float scale, int cau
   *empty = B == 0 || H == 0 || Nq == 0;
   if (*empty) return FA_OK;
   if (Hkv == 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(B) * H > 65535) return FA_ERR_UNSUPPORTED;
+  if (!batch_fits(B, H)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -708,7 +714,7 @@ fa_status fa_rope(const void* x, void* y, const int* positions, const double* in
   if (!std::isfinite(factor)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * H > 65535 || static_cast<long long>(B) * N > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  if (!batch_fits(B, H) || static_cast<long long>(B) * N > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
   if (B == 0 || H == 0 || N == 0) return FA_OK;
   if (!x || !y || !inv_freq) return FA_ERR_INVALID_ARG;
   const int sizes[3] = {B, H, N};
@@ -790,8 +796,7 @@ fa_status fa_cache_append_fp8(const void* k, const void* v, const int* slots, vo
   if (B < 0 || Hkv < 0 || N < 0 || num_pages < 0) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (!page_ok(page_size)) return FA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hkv > 65535 || static_cast<long long>(B) * N > 0x7fffffffll ||
-      !cache_fits(num_pages, Hkv, page_size) ||
+  if (!batch_fits(B, Hkv) || static_cast<long long>(B) * N > 0x7fffffffll || !cache_fits(num_pages, Hkv, page_size) ||
       static_cast<long long>(B) * ((static_cast<long long>(N) + 15) / 16) * Hkv * 2 > 0x7fffffffll)   // blocks
     return FA_ERR_UNSUPPORTED;
   if (B == 0 || Hkv == 0 || N == 0) return FA_OK;

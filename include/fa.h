@@ -306,6 +306,10 @@ FA_API size_t fa_fwd_standard_workspace_size(int B, int H, int N, int d);
  * or beyond the table counts as the nearest possible one; a page or slot
  * outside the cache is skipped (its keys count as not visible) and
  * fa_device_status then returns FA_ERR_BAD_PAGE.
+ *
+ * Limits (FA_ERR_UNSUPPORTED beyond): B * H <= 65535, or B <= 8192 and H <=
+ * 65535 (Hkv in fa_cache_append_fp8); fa_page_tables B <= 65535; B * N, num_pages
+ * * Hkv and num_pages * page_size below 2^31, max_pages * page_size up to 2^30.
  */
 
 /* Scalings of the rotary frequencies f_i = base^(-2 i / rot_dim). */

@@ -60,3 +60,26 @@ def test_lowered_lengths_lose_no_page():
         live = slots[slots >= 0]
         assert len(set(live)) == len(live)
         ctx = np.maximum(lens - rng.integers(0, 2 * N, B), 0)
+
+
+def test_batches_of_many_heads_are_not_refused():
+    """1024 requests of 64 heads (and 8192 of any number that the other limits allow) pass the host's checks of shapes."""
+    C, P = fa.STATUS_CODES, 4096
+    bad = C["FA_ERR_ALIGNMENT"]                          # q, x, k at an odd address: the check behind those of shapes
+
+    def decode(B, H, Hkv):
+        need = fa.fa_fwd_decode_paged_fp8_workspace_size(B, H, Hkv, 1, 64)
+        return fa.lib.fa_fwd_decode_paged_fp8(P + 2, P, P, P, P, P, P, P, P, B, H, Hkv, 1, 64, 9, 16, 4, 0.1, 0, P, need, None)
+
+    def rope(B, H):
+        return fa.lib.fa_rope(P + 2, 2 * P, P, P, 1.0, B, H, 1, 64, 64, 0, 0, H * 64, 64, 64, H * 64, 64, 64, None)
+
+    def append(B, Hkv):
+        return fa.lib.fa_cache_append_fp8(P + 2, P, P, P, P, P, P, B, Hkv, 1, 64, 9, 16, None)
+
+    for B, H in ((1024, 64), (1024, 256), (8192, 128), (1, 65535), (65535, 1)):
+        assert decode(B, H, H // 4 if H % 4 == 0 else H) == rope(B, H) == append(B, H) == bad, (B, H)
+    for B, H in ((8193, 8), (65536, 1), (1, 65536)):
+        assert rope(B, H) == append(B, H) == C["FA_ERR_UNSUPPORTED"], (B, H)
+        with pytest.raises(fa.FAError, match="unsupported"):
+            decode(B, H, H)

@@ -146,3 +146,22 @@ def test_page_tables_held_counts_out_of_range():
     for bad in (held_t.long(), held_t[:1], held_t.cpu(), held_t[None]):
         with pytest.raises(ValueError):
             fa.fa_page_tables(*args, held_pages=bad)
+
+
+def test_batches_of_more_heads_than_a_grid_dimension():
+    """1030 requests of 64 heads (65920) through rope, the cache write and the paged decode."""
+    rng = np.random.default_rng(205)
+    B, H, d, page = 1030, 64, 64, 16
+    x64, x = bf16(rng.standard_normal((B, H, 1, d)))
+    freq, _ = fa.rope_frequencies(d)
+    pos = rng.integers(0, 5000, (B, 1))
+    ref = paged.rope(x64, pos, freq.cpu().numpy())
+    y = gu.to_f64(fa.rope_forward(x, i32(pos), freq))
+    pair = np.tile(np.abs(x64[..., : d // 2]) + np.abs(x64[..., d // 2:]), 2)
+    assert np.all(np.abs(y - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * pair)
+    kc, ks, kct, kst = cache(rng, B, H, page, d)
+    slots = rng.permutation(B)[:, None] * page + rng.integers(0, page, (B, 1))
+    check_append(x64, x64, x, x, slots, (kc, kct), (kc, kct), (ks, kst), (ks, kst), page, H, d)
+    lens = rng.integers(0, 40, B)
+    case = decode_case(B, H, 8, 1, d, page, lens, seed=206)
+    check_decode(*case, d ** -0.5, False, d)
