@@ -13,8 +13,7 @@
 // where they fall among the type's subnormals.  A page is written by one group
 // of threads that holds all of it, 64 elements per thread (fewer where a page is
 // small), in registers: the new values are read once.  Many tokens are bound by
-// memory, 3 bytes per element (B4 Hkv8 N8192 d128, 164 MB: 32-35 us, 4.6-5.1
-// TB/s), a few by a chain of loads, slot, scale, values (B64 N1: 4.2 us, most
+// memory, 3 bytes per element (B4 Hkv8 N8192 d128, 164 MB: 33.8 us, 4.8 TB/s), a few by a chain of loads, slot, scale, values (B64 N1: 4.2 us, most
 // of it the launch).
 //
 // page_tables_kernel.  See the comment there.
@@ -34,22 +33,39 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 
-// Eight bf16 values times `inv` -> eight e4m3 codes.  With `odd`, a value that is
-// not finite becomes the type's NaN (the conversion alone makes the largest
-// value of an infinity).
-__device__ __forceinline__ uint2 quantise8(uint4 x, float inv, bool odd) {
+// x / scale with inv = 1 / scale rounded: the product, and what is left of x added
+// in the same way (one step of refinement, so that a quotient of few bits, a tie of
+// the rounding that follows among them, comes out exactly).
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, scale, x), inv, q);
+}
+// Eight bf16 values times `inv` -> eight e4m3 codes.
+__device__ __forceinline__ uint2 quantise8(uint4 x, float inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     r[i] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv),
                                     __NV_SATFINITE, __NV_E4M3);
-  if (odd)
+  return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+// The same with quotients, for a scale that is no power of two (of a cache filled
+// elsewhere); a value that is not finite becomes the type's NaN (the conversion
+// alone makes the largest value of an infinity).  A function of its own, so that
+// the common path keeps its registers: B4 Hkv8 N8192 d128 33.8 us (pages of 32
+// 33.7), inline 34.9 (38.6).
+__device__ __noinline__ uint2 quantise8_odd(uint4 x, float scale, float inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if ((w[i] & 0x7f80u) == 0x7f80u) r[i] = (r[i] & 0xff00u) | 0x7fu;
-      if ((w[i] & 0x7f800000u) == 0x7f800000u) r[i] = (r[i] & 0x00ffu) | 0x7f00u;
-    }
+  for (int i = 0; i < 4; ++i) {
+    r[i] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(__uint_as_float(w[i] << 16), scale, inv),
+                                                quotient(__uint_as_float(w[i] & 0xffff0000u), scale, inv)),
+                                    __NV_SATFINITE, __NV_E4M3);
+    if ((w[i] & 0x7f80u) == 0x7f80u) r[i] = (r[i] & 0xff00u) | 0x7fu;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) r[i] = (r[i] & 0x00ffu) | 0x7f00u;
+  }
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
@@ -227,12 +243,13 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const A
       if (!(was > 0.0f && was <= 3.0e38f)) was = 0.0f;    // no usable scale: nothing of the page is kept
       const float now = fmaxf(was, scale_for(top));
       const float inv = 1.0f / now;
+      strange |= (__float_as_uint(now) & 0x7fffffu) != 0u;
       const bool grow = !fresh && now != was;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         uint2* p = reinterpret_cast<uint2*>(codes + (i * kTpi + t) * 8);
         if ((put >> i) & 1u)
-          *p = quantise8(val[i], inv, strange);
+          *p = strange ? quantise8_odd(val[i], now, inv) : quantise8(val[i], inv);
         else if (grow)
           *p = was > 0.0f ? rescale8(*p, was * inv) : make_uint2(0u, 0u);
       }

@@ -417,8 +417,8 @@ FA_API fa_status fa_page_tables_held(const int* ctx_lens, const int* new_lens, i
  *   code  = e4m3(x / scale), round to nearest even; what is not finite is
  *           stored as NaN, what exceeds 448 * 2^60 as the largest value.
  * If the scale grows, the page's other codes become e4m3(code * old / new).
- * Scales are powers of two, so that step is exact down to the type's
- * subnormals.  An old scale that is not positive and finite keeps nothing of
+ * Scales that the call makes are powers of two, so that step is exact down to
+ * the type's subnormals; a page's old scale may be any positive number.  An old scale that is not positive and finite keeps nothing of
  * the page (its other codes become 0).
  */
 FA_API fa_status fa_cache_append_fp8(const void* k, const void* v, const int* slots, void* k_cache, void* v_cache,

@@ -108,6 +108,29 @@ def check_decode_floor(q, kc, vc, ks, vs, table, lens, scale, d, ref):
     return got
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 128])
+def test_append_to_pages_whose_scale_is_no_power_of_two(page, d):
+    """A cache that was quantised elsewhere, with any positive scale: code = e4m3(x / scale) where the scale stays, ties to
+    even included (values are scale times numbers of six bits, exact in bf16), and codes moved to a power of two where it grows."""
+    rng = np.random.default_rng(204)
+    pages = 24
+    kc, ks, kct, kst = cache(rng, pages, 1, page, d)
+    vc, vs, vct, vst = cache(rng, pages, 1, page, d)
+    for s in (ks, vs):
+        s[:] = rng.choice([0.75, 1.25, 0.625, 0.875], s.shape) * 2.0 ** rng.integers(-6, 3, s.shape)
+    upload((ks, kst), (vs, vst))
+
+    def values(scale):
+        m = rng.integers(16, 32, (pages, 1, 2, d)) * 2.0 ** rng.integers(-8, 4, (pages, 1, 2, d)) * rng.choice([-1, 1], (pages, 1, 2, d))
+        m[::3] *= 64.0                                  # these pages grow
+        return m * scale[:, :, None, None]
+
+    (k64, k), (v64, v) = bf16(values(ks)), bf16(values(vs))
+    slots = np.arange(pages)[:, None] * page + np.array([[3, 4]])
+    check_append(k64, v64, k, v, slots, (kc, kct), (vc, vct), (ks, kst), (vs, vst), page, 1, d)
+
+
 @pytest.mark.parametrize("B,N,page,pages", [(1, 5, 16, 6), (5, 40, 16, 30), (33, 3, 32, 25), (2500, 2, 16, 4000), (3, 700, 128, 40)])
 def test_page_tables_of_requests_that_shrink(B, N, page, pages):
     """Lengths lowered between calls (rejected drafts), across pages' borders too: every call as the oracle's, and no page
