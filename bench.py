@@ -443,7 +443,7 @@ def run_case(args):
             fa.fa_fwd_fp8(q8, k8, v8, 0.01, 0.01, 0.01, o, lse, d ** -0.5, args.causal, stream)
         flops = fwd_flops(B, H, N, d, args.causal)
     elif args.case == "serve":
-        step, nbytes = serve_step(args, B, H, N, d, dev, rnd)
+        step, nbytes, tokens = serve_step(args, B, H, N, d, dev, rnd)
     else:
         q, k, v = rnd(B, H, N, d), rnd(B, H, N, d), rnd(B, H, N, d)
         o = torch.empty_like(q)
@@ -467,6 +467,8 @@ def run_case(args):
         raise RuntimeError(f"device status {st} (wait site {where})")
     ms = e0.elapsed_time(e1) / args.steps
     line = {"case": args.case, "shape": args.shape, "causal": bool(args.causal), "ms_per_step": round(ms, 5)}
+    if args.case == "serve":
+        line["cached_tokens"] = tokens
     if nbytes:
         line["nq"] = args.nq
         line["gbs"] = round(nbytes / ms / 1e6, 1)
@@ -475,8 +477,14 @@ def run_case(args):
     print(json.dumps(line), flush=True)
 
 
+def serve_lengths(B, N):
+    """Lengths of the serving case's requests at first: N, and from there down to N / 2."""
+    return [N - i * (N - N // 2) // max(1, B - 1) for i in range(B)]
+
+
 def serve_step(args, B, H, N, d, dev, rnd):
-    """The captured decode step of --case serve, and the bytes of codes that its attention reads at first."""
+    """The captured decode step of --case serve, the bytes of codes that its attention reads at first, and the tokens
+    that the cache holds then."""
     import torch
 
     import exact_io_aware_55_b200 as fa
@@ -489,8 +497,9 @@ def serve_step(args, B, H, N, d, dev, rnd):
     per_row = -(-(N + grown) // page)
     pages = B * per_row
     i32 = {"dtype": torch.int32, "device": dev}
-    ctx = torch.linspace(N // 2, N, B, device=dev).to(torch.int32)
-    tokens = int(ctx.sum())
+    lengths = serve_lengths(B, N)
+    ctx = torch.tensor(lengths, **i32)
+    tokens = sum(lengths)
     free = torch.randperm(pages, device=dev).to(torch.int32)
     table = torch.full((B, per_row), -1, **i32)
     head = torch.zeros(1, **i32)
@@ -498,7 +507,7 @@ def serve_step(args, B, H, N, d, dev, rnd):
     # the cache holds the prompts already: their pages are taken, their codes drawn
     k_cache, v_cache = (torch.randint(0, 0x70, (pages, Hkv, page, d), dtype=torch.uint8, device=dev) for _ in range(2))
     k_scale, v_scale = (torch.full((pages, Hkv), 2.0 ** -6, device=dev) for _ in range(2))
-    counts = [(-(-n // page)) for n in ctx.tolist()]
+    counts = [-(-n // page) for n in lengths]
     used = 0
     for b, n in enumerate(counts):
         table[b, :n] = free[used:used + n]
@@ -523,7 +532,7 @@ def serve_step(args, B, H, N, d, dev, rnd):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         eager()
-    return graph.replay, 2 * tokens * Hkv * d
+    return graph.replay, 2 * tokens * Hkv * d, tokens
 
 
 def kernel_source_digest(files) -> str:
