@@ -395,8 +395,9 @@ def run_case(args):
     'fp8' (B,H,N,d: the e4m3 forward), 'det' (B,H,N,d: the backward with the
     deterministic dQ pass, after one forward) or 'serve' (B,H,N,d: a decode step
     of --nq tokens a request over an 8-bit paged cache of N/2 to N tokens, four
-    query heads to a KV head: page tables, rotary positions, the cache write and
-    the attention, captured into a CUDA graph; lengths grow from step to step)."""
+    query heads to a KV head: page tables, rotary positions on a fused
+    projection's output, a copy of its V, the cache write and the attention,
+    captured into a CUDA graph; lengths grow from step to step)."""
     import torch
 
     import exact_io_aware_55_b200 as fa
@@ -469,6 +470,7 @@ def run_case(args):
     line = {"case": args.case, "shape": args.shape, "causal": bool(args.causal), "ms_per_step": round(ms, 5)}
     if args.case == "serve":
         line["cached_tokens"] = tokens
+        line["inputs"] = "token-major projection"
     if nbytes:
         line["nq"] = args.nq
         line["gbs"] = round(nbytes / ms / 1e6, 1)
@@ -514,8 +516,10 @@ def serve_step(args, B, H, N, d, dev, rnd):
         used += n
     head.fill_(used)
     new = torch.full((B,), nq, **i32)
-    q, k, v = rnd(B, H, nq, d), rnd(B, Hkv, nq, d), rnd(B, Hkv, nq, d)
-    qr, kr, o = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q)
+    # a fused projection's output, token-major: rope writes its part of it out head by head, V is copied
+    qkv = rnd(B, nq, H + 2 * Hkv, d).transpose(1, 2)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    qr, kr, vr, o = (torch.empty((B, h, nq, d), dtype=torch.bfloat16, device=dev) for h in (H, Hkv, Hkv, H))
     lse = torch.empty((B, H, nq), device=dev)
     freq, factor = fa.rope_frequencies(d, device=dev)
     work = torch.empty(fa.fa_fwd_decode_paged_fp8_workspace_size(B, H, Hkv, nq, d), dtype=torch.uint8, device=dev)
@@ -524,7 +528,8 @@ def serve_step(args, B, H, N, d, dev, rnd):
         fa.fa_page_tables(ctx, new, free, head, table, slots, pos, ctx, head, page)
         fa.fa_rope(q, qr, pos, freq, factor)
         fa.fa_rope(k, kr, pos, freq, factor)
-        fa.fa_cache_append_fp8(kr, v, slots, k_cache, v_cache, k_scale, v_scale)
+        vr.copy_(v)
+        fa.fa_cache_append_fp8(kr, vr, slots, k_cache, v_cache, k_scale, v_scale)
         fa.fa_fwd_decode_paged_fp8(qr, k_cache, v_cache, k_scale, v_scale, table, ctx, o, lse, d ** -0.5, True, work)
 
     eager()
