@@ -430,6 +430,8 @@ FA_API fa_status fa_cache_append_fp8(const void* k, const void* v, const int* sl
  * attend over the first seq_lens[b] tokens of request b (the queries' own
  * tokens are in the cache and counted).  H is a multiple of Hkv; query heads
  * h * H/Hkv .. (h+1) * H/Hkv - 1 share KV head h.
+ * A chunk of a prompt behind cached tokens has no call of its own: it goes in
+ * slices of up to 16 queries, each of which reads the cache again.
  *   q           : in,  bf16 [B,H,Nq,d]
  *   o           : out, bf16 [B,H,Nq,d]
  *   lse         : out, fp32 [B,H,Nq], natural log

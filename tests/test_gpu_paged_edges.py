@@ -6,7 +6,7 @@ import torch
 
 from oracle import paged
 from tests import gpu_util as gu
-from tests.test_gpu_paged import bf16, cache, check_append, check_decode, decode_case, fa, i32
+from tests.test_gpu_paged import SCRIPT, Loop, bf16, cache, check_append, check_decode, decode_case, fa, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -188,3 +188,39 @@ def test_batches_of_more_heads_than_a_grid_dimension():
     lens = rng.integers(0, 40, B)
     case = decode_case(B, H, 8, 1, d, page, lens, seed=206)
     check_decode(*case, d ** -0.5, False, d)
+
+
+def test_decode_loop_captured_over_two_streams():
+    """A captured step whose rope calls run on a stream each, behind a memset and before a copy, and which joins them again."""
+    loop = Loop(5, 8, 2, 5, 128, 16, pages=14, per_row=3, seed=207)
+    side = torch.cuda.Stream()
+
+    def step():
+        B, H, Hkv, N, d, page = loop.shape
+        main = torch.cuda.current_stream()
+        loop.o.zero_()
+        fa.fa_page_tables(loop.ctx, loop.new, loop.free, loop.head, loop.table, loop.slots, loop.pos, loop.ctx, loop.head, page)
+        x = loop.qkv.transpose(1, 2)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            fa.fa_rope(x[:, H:H + Hkv], loop.qk[:, H:], loop.pos, loop.freq, loop.factor)
+            k = loop.qk[:, H:].contiguous()
+        fa.fa_rope(x[:, :H], loop.qk[:, :H], loop.pos, loop.freq, loop.factor)
+        q = loop.qk[:, :H].contiguous()
+        main.wait_stream(side)
+        fa.fa_cache_append_fp8(k, x[:, H + Hkv:].contiguous(), loop.slots, loop.kc, loop.vc, loop.ks, loop.vs)
+        fa.fa_fwd_decode_paged_fp8(q, loop.kc, loop.vc, loop.ks, loop.vs, loop.table, loop.ctx, loop.o, loop.lse, d ** -0.5, True, loop.work)
+
+    loop.load([0] * 5)
+    first = torch.cuda.Stream()
+    first.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(first):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for new in SCRIPT:
+        loop.load(new)
+        graph.replay()
+        loop.check()
