@@ -772,10 +772,10 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
     for (int t0 = 0; t0 < n_tiles && ok; t0 += pb.tiles) {
       const int next = pb.fetch();
       const int m = min(pb.tiles, n_tiles - t0);
-      // at least 2^-60 (the values of a scale of 0 are cleared); a NaN stays one, and
-      // the logarithm makes one of a negative scale
-      const float v = vs >= 0.0f ? fmaxf(vs, 8.673617379884035e-19f) : vs;
-      const float lv = log2f(v), iv = vs >= 0.0f ? 1.0f / v : 1.0f;   // finite: it meets p = 0 of rows that do not see the page
+      const float v = fmaxf(vs, 8.673617379884035e-19f);     // 2^-60; the values of a scale of 0 are cleared
+      // a NaN or negative scale shows in the scores (1 / v stays finite: it meets
+      // p = 0 of rows that do not see the page)
+      const float lv = vs >= 0.0f ? log2f(v) : NAN, iv = 1.0f / v;
       for (int u = 0; u < m; ++u) {
         if (left == 0) {
           pc = coming;
