@@ -13,8 +13,10 @@
 // where they fall among the type's subnormals.  A page is written by one group
 // of threads that holds all of it, 64 elements per thread (fewer where a page is
 // small), in registers: the new values are read once.  Many tokens are bound by
-// memory, 3 bytes per element (B4 Hkv8 N8192 d128, 164 MB: 33.8 us, 4.8 TB/s), a few by a chain of loads, slot, scale, values (B64 N1: 4.2 us, most
-// of it the launch).
+// memory, 3 bytes per element (B4 Hkv8 N8192 d128, 164 MB: 33.8 us among others,
+// 4.8 TB/s, 37 alone), and by loads of which each waits for the one before: slot,
+// scale, values.  A few tokens are that chain (B64 N1: 4.2 us, most of it the
+// launch).
 //
 // page_tables_kernel.  See the comment there.
 #include <cooperative_groups.h>

@@ -51,13 +51,13 @@
 // that are not there, since p = 0 times a stale NaN code would be NaN.
 //
 // Measured, in a CUDA graph, H/Hkv = 4, ragged lengths up to n: B32 Hkv8 n8192
-// d128 57 us with pages of 16, 54 with 64 (301 MB, 5.3 and 5.6 TB/s; loads alone
-// 49); B8 n131072 177 us (6.65 TB/s).  32 rows (B48 Hkv8, 4 queries of 8 heads,
-// n16384, 909 MB) 183 us, 5.0 TB/s: the softmax warps issue on most cycles and
-// wait for one another's tiles (loads alone 132; under a sustained load at 1.68
-// GHz 230 us).  What short pieces cost is the chain from pages to output, about
-// 10 us from launch to end: B1 n1000 12.4 us, of which the launch, lengths,
-// table and first tile are 6.
+// d128 56 us with pages of 16, 53 with 64 (300 MB, 5.4 and 5.7 TB/s; loads alone
+// 49); B8 n131072 125 and 120 us (772 MB, 6.2 and 6.4 TB/s).  32 rows (B48 Hkv8,
+// 4 queries of 8 heads, n16384, 965 MB) 199 us, 4.9 TB/s: half of the issue slots
+// are used, the softmax warps wait for S, which each loads and needs at once, and
+// for one another (under a sustained load at lower clocks 230 us).  What short
+// pieces cost is the chain from pages to output, about 10 us from launch to end:
+// B1 n1000 12.4 us, of which the launch, lengths, table and first tile are 6.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
