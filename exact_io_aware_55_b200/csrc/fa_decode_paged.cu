@@ -1077,8 +1077,11 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
       const int rows = min(R, a.rows - row0);
       const size_t out = (static_cast<size_t>(pc.b) * a.Hkv + hk) * a.rows + row0;
       // lane r has row r's sum, and the factor of each turn's O: a turn without a
-      // visible key has none (its O may never have been written)
-      float f[S::kTurns] = {};
+      // visible key has none, -1 (its O may never have been written); a factor of 0
+      // counts, so that a NaN among the values shows
+      float f[S::kTurns];
+#pragma unroll
+      for (int k = 0; k < S::kTurns; ++k) f[k] = -1.0f;
       if (ok && lane < rows) {
         float M = -INFINITY, L = 0.0f;
 #pragma unroll
@@ -1086,12 +1089,15 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < S::kTurns; ++k) {
           const float m = b->stat_m[ob][k][lane];
-          f[k] = m == -INFINITY ? 0.0f : ex2_approx(m - M);
-          L = fmaf(f[k], b->stat_l[ob][k][0][lane] + b->stat_l[ob][k][1][lane] + b->stat_l[ob][k][2][lane] + b->stat_l[ob][k][3][lane], L);
+          const float l = b->stat_l[ob][k][0][lane] + b->stat_l[ob][k][1][lane] + b->stat_l[ob][k][2][lane] + b->stat_l[ob][k][3][lane];
+          const float x = m == -INFINITY ? 0.0f : ex2_approx(m - M);
+          if (m != -INFINITY || l != 0.0f) f[k] = x;    // without a maximum the sum is 0 or NaN
+          L = fmaf(x, l, L);
         }
         const float inv = L == 0.0f ? 0.0f : b->stat_ref[ob] * (1.0f / kBase) / L;
 #pragma unroll
-        for (int k = 0; k < S::kTurns; ++k) f[k] *= inv;
+        for (int k = 0; k < S::kTurns; ++k)
+          if (!(f[k] < 0.0f)) f[k] *= inv;
         if (wq == 0) {
           const float lse = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
           if (whole)
@@ -1133,7 +1139,7 @@ __global__ void __launch_bounds__(PgShape<D, R>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kStep; ++k) {
             const float w = __shfl_sync(0xffffffffu, f[t], rg + k);
-            const float y = w == 0.0f ? 0.0f : v[k] * w;
+            const float y = w < 0.0f ? 0.0f : v[k] * w;
             o[k] = t == 0 ? y : o[k] + y;
           }
         }

@@ -224,3 +224,46 @@ def test_decode_loop_captured_over_two_streams():
         loop.load(new)
         graph.replay()
         loop.check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H", [2, 8, 32])
+def test_decode_nan_value_of_a_key_far_below_the_others(H, d):
+    """The first tile's scores lie 300 below the second's, so that its weights are 0 in fp32: a NaN among its values shows all
+    the same (0 times NaN), whichever way the two tiles are joined."""
+    B, tile = 60, 128 if d == 128 else 256
+    q, kc, vc, ks, vs, table, lens = decode_case(B, H, 2, 1, d, 16, [2 * tile] * B, seed=208, stale=False)
+    q[0][:] = 0.0
+    q[0][..., 0] = 1.0
+    kc[0][..., 0] = 0x7E                                # 448, and -448 in the first tile
+    kc[0][table[:, : tile // 16], :, :, 0] = 0xFE
+    ks[0][:] = 2.0 ** -3
+    vc[0][table[::3, 1], 1, 5, 7] = 0x7F
+    upload((kc[0], kc[1]), (vc[0], vc[1]), (ks[0], ks[1]))
+    q[1].copy_(torch.from_numpy(q[0]))
+    scale = 300.0 / 112.0
+    ref = paged.decode_paged(q[0], kc[0], vc[0], ks[0], vs[0], table, lens, scale, False)
+    assert np.isnan(ref[0][::3, H // 2:, :, 7]).all() and np.isnan(ref[0]).sum() == 20 * (H // 2)
+    check_decode(q, kc, vc, ks, vs, table, lens, scale, False, d, want=ref)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_decode_drawn_nan_and_skipped_pages(seed):
+    """NaN in queries, keys and values and pages outside the cache, drawn at random together: NaN where the definition has it."""
+    rng = np.random.default_rng(300 + seed)
+    d, page, causal = int(rng.choice([64, 128])), int(rng.choice([16, 32, 64])), bool(rng.integers(2))
+    Hkv, group, Nq, B = int(rng.integers(1, 4)), int(rng.choice([1, 3, 4, 8])), int(rng.integers(1, 9)), int(rng.integers(1, 30))
+    lens = [int(2 ** rng.uniform(0, 10)) for _ in range(B)]
+    q, kc, vc, ks, vs, table, n = decode_case(B, group * Hkv, Hkv, Nq, d, page, lens, seed=int(rng.integers(2 ** 31)), stale=False)
+    skipped = rng.random(table.shape) < 0.1
+    kc[0][rng.random(kc[0].shape) < 2e-5] = 0x7F
+    vc[0][rng.random(vc[0].shape) < 1e-4] = 0xFF
+    table[skipped] = rng.choice([-1, 10 ** 8], skipped.sum())
+    bad = rng.random(q[0].shape) < 1e-3
+    q[0][bad] = np.nan
+    q[1][torch.from_numpy(bad).cuda()] = float("nan")
+    upload((kc[0], kc[1]), (vc[0], vc[1]))
+    with np.errstate(invalid="ignore"):
+        ref = paged.decode_paged(q[0], kc[0], vc[0], ks[0], vs[0], table, n, d ** -0.5, causal)
+    check_decode(q, kc, vc, ks, vs, table, n, d ** -0.5, causal, d, want=ref)
+    fa.fa_device_status()
